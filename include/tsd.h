@@ -398,6 +398,65 @@ int tsd_kv_commit(void *k_cache, void *v_cache, const int32_t *prefix_len,
                   tsd_stream_t stream);
 
 /*
+ * The same commit over a paged KV cache (pools and block table as for
+ * tsd_tree_attention_paged): the K and V rows at logical positions
+ * P_b + out_path[b][i] move to P_b + i, within and across pages, every
+ * source read before any row is written.  The block table does not change;
+ * pages that no accepted row reaches any more stay the caller's to reuse.
+ * The pages of the rows that move belong to this sequence alone (a page
+ * shared with another sequence must hold prefix positions only).
+ * A sequence whose path is malformed or reaches past max_blocks * page_size
+ * sets TSD_DEV_BAD_PATH, one with a block-table entry outside
+ * [0, num_pages) for a row that moves sets TSD_DEV_BAD_PAGE; either moves
+ * nothing and keeps new_prefix_len[b] = P_b.  new_prefix_len may not be
+ * prefix_len itself.  Other arguments and errors as for tsd_kv_commit, and
+ * TSD_ERR_SHAPE for page sizes as for tsd_tree_attention_paged.
+ */
+int tsd_kv_commit_paged(void *k_pages, void *v_pages, const int32_t *block_table, int num_pages,
+                        int page_size, int max_blocks, const int32_t *prefix_len,
+                        const int32_t *out_path, const int32_t *n_accepted, int B, int Tmax,
+                        int Hkv, int D, int dtype, int32_t *new_prefix_len, int32_t *dev_status,
+                        tsd_stream_t stream);
+
+/*
+ * Rotary positions of new tokens, appended to a paged KV cache (no
+ * counterpart in the pages: the step in front of tree or chunk attention).
+ * For every sequence b and slot u < n_new[b] <= Tmax the token's position is
+ * pos = P_b + u, or P_b + depth[b][u] - 1 when depth is given (a token tree:
+ * depth as written by tsd_tree_mask_build), and pair i < rot_dim / 2 of each
+ * head of q and k turns by the angle pos * inv_freq[i]:
+ *     (x, y) -> rot_scale * (x cos - y sin, y cos + x sin)
+ * with pairs (i, i + rot_dim / 2), or (2i, 2i + 1) when interleaved != 0;
+ * dimensions from rot_dim on are copied.  Then
+ *     q_out[b][u]          = the rotated q rows (dense),
+ *     cache position P_b+u = the rotated k rows and the v rows.
+ *   q, k, v    [B][Tmax][Hq or Hkv][D] dtype; a token's rows are dense,
+ *              *_token and *_batch are the elements from one token, and from
+ *              one sequence, to the next (so that all three may be columns of
+ *              one projection)
+ *   inv_freq   [rot_dim / 2] fp64, radians per position
+ *   k_pages, v_pages, block_table   as for tsd_tree_attention_paged
+ * The angle is formed and reduced in fp64; cosine, sine and the rotation are
+ * fp32; every output is rounded once.  Slots u >= n_new[b] are neither read
+ * nor written.  q_out may not overlap q, k or v, and no two live slots may
+ * share a cache row.  rot_dim is even and at most D; D * element size is a
+ * multiple of 16 and at most 512 bytes; pointers and strides are multiples of
+ * 16 bytes.  Host errors: TSD_ERR_NULL, TSD_ERR_SHAPE, TSD_ERR_DTYPE,
+ * TSD_ERR_ALIGN, TSD_ERR_CUDA.  Device: TSD_DEV_BAD_PREFIX (n_new[b] outside
+ * [0, Tmax], or P_b + n_new[b] outside the table's positions: nothing of that
+ * sequence is written), TSD_DEV_BAD_PAGE (a block-table entry outside
+ * [0, num_pages): that token's K and V rows are not written).
+ */
+int tsd_rope_append_paged(const void *q, int64_t q_batch, int64_t q_token, const void *k,
+                          int64_t k_batch, int64_t k_token, const void *v, int64_t v_batch,
+                          int64_t v_token, const double *inv_freq, int rot_dim, int interleaved,
+                          float rot_scale, const int32_t *prefix_len, const int32_t *n_new,
+                          const int32_t *depth, int B, int Tmax, int Hq, int Hkv, int D, int dtype,
+                          void *q_out, void *k_pages, void *v_pages, const int32_t *block_table,
+                          int num_pages, int page_size, int max_blocks, int32_t *dev_status,
+                          tsd_stream_t stream);
+
+/*
  * Self-test of the bounded waits (no counterpart in the paper).  Every wait
  * in the kernels above gives up after a time limit, sets TSD_DEV_TIMEOUT and
  * returns, so that a stalled pipeline ends with a status instead of a hung

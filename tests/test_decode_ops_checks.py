@@ -1,0 +1,149 @@
+"""Argument checks and host arithmetic of the decoding-loop operators (CPU only).
+
+The library is replaced by a stand-in that records the calls, as in
+test_binding_checks; the C entry points' own checks run on fake addresses,
+which never reach a launch.
+"""
+
+import math
+
+import pytest
+import torch
+
+import tree_speculative_decoding_ancestor_b200 as tsd
+from test_binding_checks import lib  # noqa: F401  (fixture)
+
+i32 = dict(dtype=torch.int32)
+bf = dict(dtype=torch.bfloat16)
+B, T, Hq, Hkv, D, page = 2, 5, 4, 2, 64, 16
+
+
+def _cache(dtype=torch.bfloat16):
+    return dict(k_pages=torch.zeros(6, Hkv, page, D, dtype=dtype),
+                v_pages=torch.zeros(6, Hkv, page, D, dtype=dtype),
+                block_table=torch.zeros(B, 3, **i32))
+
+
+def _rope(**kw):
+    a = dict(q=torch.zeros(B, T, Hq, D, **bf), k=torch.zeros(B, T, Hkv, D, **bf),
+             v=torch.zeros(B, T, Hkv, D, **bf), inv_freq=torch.ones(D // 2, dtype=torch.float64),
+             prefix_len=torch.zeros(B, **i32), n_new=torch.zeros(B, **i32), **_cache())
+    a.update(kw)
+    return tsd.rope_append_paged(**a)
+
+
+def _commit(**kw):
+    a = dict(prefix_len=torch.zeros(B, **i32),
+             result=tsd.VerifyResult(torch.zeros(B, T + 1, **i32), torch.zeros(B, T, **i32),
+                                     torch.zeros(B, **i32)), **_cache())
+    a.update(kw)
+    return tsd.kv_commit_paged(**a)
+
+
+def test_rope_arguments(lib):  # noqa: F811
+    assert _rope().shape == (B, T, Hq, D)
+    qkv = torch.zeros(B, T, Hq + 2 * Hkv, D, **bf)
+    _rope(q=qkv[:, :, :Hq], k=qkv[:, :, Hq:Hq + Hkv], v=qkv[:, :, Hq + Hkv:],
+          depth=torch.ones(B, T, **i32))
+    n = len(lib.calls)
+    with pytest.raises(ValueError):     # heads interleaved inside a token
+        _rope(q=torch.zeros(B, T, D, Hq, **bf).transpose(2, 3))
+    with pytest.raises(TypeError):
+        _rope(inv_freq=torch.ones(D // 2))
+    with pytest.raises(TypeError):
+        _rope(k=torch.zeros(B, T, Hkv, D))
+    with pytest.raises(ValueError):
+        _rope(v=torch.zeros(B, T + 1, Hkv, D, **bf))
+    with pytest.raises(ValueError):
+        _rope(block_table=torch.zeros(B + 1, 3, **i32))
+    with pytest.raises(TypeError):
+        _rope(q=torch.zeros(B, T, Hq, D, dtype=torch.float16))
+    with pytest.raises(TypeError):
+        _rope(k_pages=torch.zeros(6, Hkv, page, D))
+    q = torch.zeros(B, T, Hq, D, **bf)
+    with pytest.raises(ValueError, match="overlap"):
+        _rope(q=q, out=q)
+    with pytest.raises(ValueError):
+        _rope(depth=torch.ones(B, T - 1, **i32))
+    assert len(lib.calls) == n
+
+
+def test_commit_arguments(lib):  # noqa: F811
+    assert _commit().shape == (B,)
+    n = len(lib.calls)
+    P = torch.zeros(B, **i32)
+    with pytest.raises(ValueError, match="overlap"):
+        _commit(prefix_len=P, new_prefix_len=P)
+    with pytest.raises(ValueError):
+        _commit(v_pages=torch.zeros(5, Hkv, page, D, **bf))
+    with pytest.raises(TypeError):
+        _commit(block_table=torch.zeros(B, 3, dtype=torch.int64))
+    assert len(lib.calls) == n
+
+
+def test_host_tensors_are_refused():
+    for call in (_rope, _commit):
+        with pytest.raises(ValueError, match="CUDA device"):
+            call()
+
+
+_A, _U = 0x10000, 0x10004   # an aligned and a misaligned stand-in address
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="fake addresses must not reach a GPU")
+def test_c_entry_points_refuse():
+    NULL, SHAPE, DTYPE, ALIGN = -1, -2, -3, -6
+    L = tsd.load_library()
+
+    def rope(q=_A, qs=(256, 256), rot=64, B=2, T=4, Hq=4, Hkv=2, D=64, dt=1, k=_A, table=_A, ps=16,
+             inv=_A, out=_A):
+        return L.tsd_rope_append_paged(q, *qs, k, 128, 128, _A, 128, 128, inv, rot, 0, 1.0, _A, _A,
+                                       None, B, T, Hq, Hkv, D, dt, out, _A, _A, table, 4, ps, 2, None,
+                                       None)
+    assert rope(B=0) == 0
+    for bad in (dict(q=None), dict(k=None), dict(table=None), dict(inv=None), dict(out=None)):
+        assert rope(**bad) == NULL
+    for bad in (dict(rot=0), dict(rot=3), dict(rot=66), dict(D=60), dict(B=-1), dict(T=0), dict(ps=24),
+                dict(qs=(256, 255)), dict(qs=(-256, 256)), dict(Hkv=0), dict(B=70000)):
+        assert rope(**bad) == SHAPE
+    assert rope(dt=2) == DTYPE
+    assert rope(q=_U) == ALIGN and rope(qs=(260, 260)) == ALIGN and rope(out=_U) == ALIGN
+
+    def commit(k=_A, D=128, dt=1, B=2, path=_A, table=_A, ps=16, blocks=2, T=8):
+        return L.tsd_kv_commit_paged(k, _A, table, 4, ps, blocks, _A, path, _A, B, T, 2, D, dt, _A,
+                                     None, None)
+    assert commit(B=0) == 0
+    for bad in (dict(k=None), dict(path=None), dict(table=None)):
+        assert commit(**bad) == NULL
+    for bad in (dict(D=4), dict(D=512), dict(ps=8), dict(blocks=0), dict(T=129), dict(B=70000),
+                dict(D=1 << 30)):
+        assert commit(**bad) == SHAPE
+    assert commit(dt=7) == DTYPE
+    assert commit(k=_U) == ALIGN
+
+
+def test_rope_frequencies():
+    f = tsd.rope_frequencies(64)
+    assert f.rot_scale == 1.0 and f.inv_freq.dtype == torch.float64
+    want = [10000.0 ** (-2 * i / 64) for i in range(32)]
+    assert torch.allclose(f.inv_freq, torch.tensor(want, dtype=torch.float64), rtol=1e-14, atol=0)
+    assert torch.allclose(tsd.rope_frequencies(64, scaling="linear", factor=4.0).inv_freq * 4,
+                          f.inv_freq, rtol=1e-15, atol=0)
+    n = tsd.rope_frequencies(64, scaling="ntk", factor=8.0).inv_freq
+    assert n[0] == 1.0 and math.isclose(float(n[-1] * 8), float(f.inv_freq[-1]), rel_tol=1e-13)
+    p = tsd.rope_frequencies(64, scaling="by_parts", factor=8.0, original_len=4096, low=1, high=32,
+                             rot_scale=1.2)
+    turns = 4096 * f.inv_freq / (2 * math.pi)
+    ratio = p.inv_freq / f.inv_freq
+    assert p.rot_scale == 1.2
+    assert torch.equal(ratio[turns >= 32], torch.ones(int((turns >= 32).sum()), dtype=torch.float64))
+    assert torch.allclose(ratio[turns <= 1], torch.full((int((turns <= 1).sum()),), 1 / 8,
+                                                         dtype=torch.float64), rtol=1e-15, atol=0)
+    mid = (turns > 1) & (turns < 32)
+    assert mid.any() and ((ratio[mid] > 1 / 8) & (ratio[mid] < 1)).all()
+    assert (ratio.diff() <= 0).all()
+    for bad in (dict(rot_dim=3), dict(rot_dim=64, base=1.0), dict(rot_dim=64, factor=0.5),
+                dict(rot_dim=64, scaling="by_parts", factor=2.0), dict(rot_dim=2, scaling="ntk"),
+                dict(rot_dim=64, scaling="other")):
+        with pytest.raises(ValueError):
+            tsd.rope_frequencies(**bad)

@@ -17,6 +17,7 @@ Six operations, each a thin wrapper over the C ABI of ``lib/libtsd.so``
 
 from .binding import (  # noqa: F401
     LIB_PATH,
+    RopeFrequencies,
     TsdError,
     Tree,
     TreeMask,
@@ -26,8 +27,11 @@ from .binding import (  # noqa: F401
     device_status,
     exported_symbols,
     kv_commit,
+    kv_commit_paged,
     launch_count,
     load_library,
+    rope_append_paged,
+    rope_frequencies,
     tree_attention,
     tree_attention_paged,
     tree_dfs_order,

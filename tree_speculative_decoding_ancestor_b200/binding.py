@@ -9,7 +9,9 @@ raises.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 import os
 import threading
 from typing import Dict, NamedTuple, Optional, Tuple
@@ -33,6 +35,7 @@ _lib: Optional[ctypes.CDLL] = None
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
 
 # name -> (restype, argtypes), mirroring include/tsd.h
@@ -60,6 +63,11 @@ _SIGNATURES: Dict[str, Tuple[object, list]] = {
     "tsd_tree_expand": (_I, [_P, _I, _I, _P, _I, _P, _P, _P, _P, _P, _I, _I, _P, _P]),
     "tsd_tree_dfs_order": (_I, [_P, _P, _P, _P, _I, _I, _P, _P, _P, _P, _P, _P]),
     "tsd_tree_merge_chains": (_I, [_P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P]),
+    "tsd_kv_commit_paged": (_I, [_P, _P, _P, _I, _I, _I, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P,
+                                 _P]),
+    "tsd_rope_append_paged": (_I, [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I, _I,
+                                   ctypes.c_float, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P,
+                                   _P, _I, _I, _I, _P, _P]),
     "tsd_debug_wait_probe": (_I, [_I, ctypes.c_ulonglong, _P, _P, _P]),
 }
 
@@ -127,6 +135,22 @@ def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape: Tuple[int, ...]
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+
+
+def _on(device: torch.device):
+    """The library launches on the current device: make it the tensors' own."""
+    return torch.cuda.device(device) if device.type == "cuda" else contextlib.nullcontext()
+
+
+def _apart(out: torch.Tensor, name: str, *inputs: torch.Tensor) -> None:
+    """Refuse a dense output that shares memory with an input."""
+    lo, hi = out.data_ptr(), out.data_ptr() + out.numel() * out.element_size()
+    for t in inputs:
+        if not t.numel() or lo == hi:
+            continue
+        span = 1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+        if t.data_ptr() < hi and lo < t.data_ptr() + span * t.element_size():
+            raise ValueError(f"{name} must not overlap an input")
 
 
 # Per-device status word and workspace cache ---------------------------------
@@ -458,6 +482,170 @@ def kv_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, prefix_len: torch.Te
                            _ptr(new_prefix_len), _ptr(st), _stream(dev))
     _check(rc, "tsd_kv_commit")
     return new_prefix_len
+
+
+def _pools(k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor,
+           dtype: torch.dtype, B: int, D: int, device: torch.device) -> Tuple[int, int, int, int]:
+    """Check the pools [num_pages][Hkv][page_size][D] and the block table
+    [B][max_blocks]; returns (num_pages, Hkv, page_size, max_blocks)."""
+    if k_pages.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("k_pages must be [num_pages][Hkv][page_size][D] and block_table "
+                         "[B][max_blocks]")
+    num_pages, Hkv, page_size, _ = k_pages.shape
+    max_blocks = block_table.shape[1]
+    _need(k_pages, "k_pages", dtype, (num_pages, Hkv, page_size, D), device)
+    _need(v_pages, "v_pages", dtype, (num_pages, Hkv, page_size, D), device)
+    _need(block_table, "block_table", torch.int32, (B, max_blocks), device)
+    return num_pages, Hkv, page_size, max_blocks
+
+
+def kv_commit_paged(k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor,
+                    prefix_len: torch.Tensor, result: VerifyResult,
+                    new_prefix_len: Optional[torch.Tensor] = None,
+                    status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """kv_commit over a paged KV cache: the accepted nodes' K/V rows move (in
+    place, within and across pages) to the logical positions right after each
+    sequence's prefix; returns the new prefix lengths [B] int32."""
+    lib = load_library()
+    dev = k_pages.device
+    _cuda(dev)
+    dt = {torch.float32: TSD_F32, torch.bfloat16: TSD_BF16}.get(k_pages.dtype)
+    if dt is None:
+        raise TypeError("k_pages must be float32 or bfloat16")
+    B, Tmax = result.out_path.shape
+    D = k_pages.shape[-1]
+    num_pages, Hkv, page_size, max_blocks = _pools(k_pages, v_pages, block_table, k_pages.dtype,
+                                                   B, D, dev)
+    _need(prefix_len, "prefix_len", torch.int32, (B,), dev)
+    _need(result.out_path, "out_path", torch.int32, (B, Tmax), dev)
+    _need(result.n_accepted, "n_accepted", torch.int32, (B,), dev)
+    if new_prefix_len is None:
+        new_prefix_len = torch.empty((B,), dtype=torch.int32, device=dev)
+    _need(new_prefix_len, "new_prefix_len", torch.int32, (B,), dev)
+    _apart(new_prefix_len, "new_prefix_len", prefix_len)
+    st = _status_for(dev, status)
+    with _on(dev):
+        rc = lib.tsd_kv_commit_paged(_ptr(k_pages), _ptr(v_pages), _ptr(block_table), num_pages,
+                                     page_size, max_blocks, _ptr(prefix_len),
+                                     _ptr(result.out_path), _ptr(result.n_accepted), B, Tmax, Hkv,
+                                     D, dt, _ptr(new_prefix_len), _ptr(st), _stream(dev))
+    _check(rc, "tsd_kv_commit_paged")
+    return new_prefix_len
+
+
+class RopeFrequencies(NamedTuple):
+    inv_freq: torch.Tensor   # [rot_dim / 2] float64, radians per position
+    rot_scale: float         # factor on cosine and sine
+
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[str] = None,
+                     factor: float = 1.0, original_len: int = 0, low: float = 1.0,
+                     high: float = 32.0, rot_scale: Optional[float] = None,
+                     device=None) -> RopeFrequencies:
+    """Rotary frequencies f_i = base^(-2i / rot_dim), computed once in fp64
+    and scaled for contexts `factor` times as long as the trained one:
+
+    * None: as they are;
+    * "linear": f_i / factor (positions interpolated);
+    * "ntk": the base grows to base * factor^(rot_dim / (rot_dim - 2)), so the
+      fastest pair keeps its frequency and the slowest is divided by factor;
+    * "by_parts": a pair that turns r = original_len * f_i / (2 pi) times over
+      the trained context keeps its frequency for r >= high, is divided by
+      factor for r <= low, and is mixed linearly in r between.
+
+    rot_scale multiplies cosine and sine (so attention logits by its square):
+    1 unless given."""
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError("rot_dim must be even and at least 2")
+    if not base > 1.0 or not factor >= 1.0:
+        raise ValueError("base must exceed 1 and factor be at least 1")
+    i = torch.arange(rot_dim // 2, dtype=torch.float64)
+    if scaling == "ntk":
+        if rot_dim < 4:
+            raise ValueError("ntk scaling needs rot_dim >= 4")
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    freq = base ** (-2.0 * i / rot_dim)
+    if scaling == "linear":
+        freq = freq / factor
+    elif scaling == "by_parts":
+        if original_len < 1 or not 0 <= low < high:
+            raise ValueError("by_parts scaling needs original_len >= 1 and 0 <= low < high")
+        keep = ((original_len * freq / (2.0 * math.pi) - low) / (high - low)).clamp(0.0, 1.0)
+        freq = freq * (keep + (1.0 - keep) / factor)
+    elif scaling not in (None, "ntk"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return RopeFrequencies(freq.to(device) if device is not None else freq,
+                           1.0 if rot_scale is None else float(rot_scale))
+
+
+def _need_rows(t: torch.Tensor, name: str, dtype: torch.dtype, shape: Tuple[int, ...],
+               device: torch.device) -> None:
+    """As _need, but only each token's rows [H][D] must be dense."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if (t.shape[3] > 1 and t.stride(3) != 1) or (t.shape[2] > 1 and t.stride(2) != t.shape[3]):
+        raise ValueError(f"{name}: the rows of a token must be contiguous")
+
+
+def _strides(t: torch.Tensor) -> Tuple[int, int]:
+    """Elements from one sequence and one token to the next ([B][T][H][D]); a
+    dimension of one has no step, and gets the dense one."""
+    row = t.shape[2] * t.shape[3]
+    token = t.stride(1) if t.shape[1] > 1 else row
+    return (t.stride(0) if t.shape[0] > 1 else t.shape[1] * token), token
+
+
+def rope_append_paged(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, inv_freq: torch.Tensor,
+                      k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor,
+                      prefix_len: torch.Tensor, n_new: torch.Tensor,
+                      depth: Optional[torch.Tensor] = None, interleaved: bool = False,
+                      rot_scale: float = 1.0, out: Optional[torch.Tensor] = None,
+                      status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Rotate q and k of the new tokens (q [B][Tmax][Hq][D], k and v
+    [B][Tmax][Hkv][D], possibly columns of one projection) by their positions
+    and append k and v to the paged cache at P_b + u; returns the rotated q
+    rows.  Positions are P_b + u, or P_b + depth[b][u] - 1 for a token tree
+    (depth of tree_mask_build).  inv_freq [rot_dim / 2] float64 comes from
+    rope_frequencies."""
+    lib = load_library()
+    dev = q.device
+    _cuda(dev)
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q must be [B][Tmax][Hq][D] and k, v [B][Tmax][Hkv][D]")
+    B, Tmax, Hq, D = q.shape
+    dt = {torch.float32: TSD_F32, torch.bfloat16: TSD_BF16}.get(q.dtype)
+    if dt is None:
+        raise TypeError("q must be float32 or bfloat16")
+    num_pages, Hkv, page_size, max_blocks = _pools(k_pages, v_pages, block_table, q.dtype, B, D,
+                                                   dev)
+    _need_rows(q, "q", q.dtype, (B, Tmax, Hq, D), dev)
+    _need_rows(k, "k", q.dtype, (B, Tmax, Hkv, D), dev)
+    _need_rows(v, "v", q.dtype, (B, Tmax, Hkv, D), dev)
+    _need(inv_freq, "inv_freq", torch.float64, (inv_freq.numel(),), dev)
+    _need(prefix_len, "prefix_len", torch.int32, (B,), dev)
+    _need(n_new, "n_new", torch.int32, (B,), dev)
+    if depth is not None:
+        _need(depth, "depth", torch.int32, (B, Tmax), dev)
+    if out is None:
+        out = torch.empty((B, Tmax, Hq, D), dtype=q.dtype, device=dev)
+    _need(out, "out", q.dtype, (B, Tmax, Hq, D), dev)
+    _apart(out, "out", q, k, v, k_pages, v_pages)
+    st = _status_for(dev, status)
+    with _on(dev):
+        rc = lib.tsd_rope_append_paged(
+            _ptr(q), *_strides(q), _ptr(k), *_strides(k), _ptr(v), *_strides(v), _ptr(inv_freq),
+            2 * inv_freq.numel(), int(bool(interleaved)), float(rot_scale), _ptr(prefix_len),
+            _ptr(n_new), _ptr(depth), B, Tmax, Hq, Hkv, D, dt, _ptr(out), _ptr(k_pages),
+            _ptr(v_pages), _ptr(block_table), num_pages, page_size, max_blocks, _ptr(st),
+            _stream(dev))
+    _check(rc, "tsd_rope_append_paged")
+    return out
 
 
 def tree_attention_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,

@@ -59,6 +59,33 @@ int check_attn(const tsd::AttnArgs &a)
     return TSD_OK;
 }
 
+// Sizes of a paged cache: a power-of-two page of 16 .. 4096 positions, at
+// most 2^30 logical positions a sequence.
+bool page_sizes_ok(int num_pages, int page_size, int max_blocks)
+{
+    return page_size >= 16 && page_size <= 4096 && (page_size & (page_size - 1)) == 0 &&
+           max_blocks >= 1 && num_pages >= 1 && (long long)max_blocks * page_size <= (1LL << 30);
+}
+
+tsd::KvPages kv_pages(const int32_t *block_table, int num_pages, int page_size, int max_blocks)
+{
+    tsd::KvPages pages;
+    pages.table = block_table;
+    pages.max_blocks = max_blocks;
+    pages.page_size = page_size;
+    pages.log2_page = __builtin_ctz((unsigned)page_size);
+    pages.num_pages = num_pages;
+    return pages;
+}
+
+// Cache rows the copying kernels move as 16-byte vectors: 0 when D elements
+// of dtype are not a multiple of 16 bytes or exceed 512.
+int cache_row_bytes(int D, int dtype)
+{
+    const int es = dtype == TSD_F32 ? 4 : 2;
+    return D >= 1 && D <= 256 && D * es % 16 == 0 && D * es <= 512 ? D * es : 0;
+}
+
 }  // namespace
 
 extern "C" {
@@ -164,19 +191,14 @@ int tsd_tree_attention_paged(const void *q, const void *k_pages, const void *v_p
                              size_t workspace_bytes, int32_t *dev_status, tsd_stream_t stream)
 {
     TSD_NVTX_RANGE();
-    if (page_size < 16 || page_size > 4096 || (page_size & (page_size - 1)) != 0 ||
-        max_blocks < 1 || num_pages < 1 || (long long)max_blocks * page_size > (1LL << 30))
+    if (!page_sizes_ok(num_pages, page_size, max_blocks))
         return TSD_ERR_SHAPE;
     tsd::AttnArgs a;
     a.q = q; a.k = k_pages; a.v = v_pages; a.prefix_len = prefix_len; a.n_nodes = n_nodes;
     a.mask = mask; a.B = B; a.Tmax = Tmax; a.Hq = Hq; a.Hkv = Hkv; a.D = D;
     a.Lmax = max_blocks * page_size;
     a.dtype = dtype; a.scale = scale; a.out = out; a.dev_status = dev_status;
-    a.pages.table = block_table;
-    a.pages.max_blocks = max_blocks;
-    a.pages.page_size = page_size;
-    a.pages.log2_page = __builtin_ctz((unsigned)page_size);
-    a.pages.num_pages = num_pages;
+    a.pages = kv_pages(block_table, num_pages, page_size, max_blocks);
     if (B == 0)
         return TSD_OK;
     if (!block_table)
@@ -284,18 +306,94 @@ int tsd_kv_commit(void *k_cache, void *v_cache, const int32_t *prefix_len,
         return TSD_ERR_SHAPE;
     if (dtype != TSD_F32 && dtype != TSD_BF16)
         return TSD_ERR_DTYPE;
-    const int row_bytes = D * (dtype == TSD_F32 ? 4 : 2);
-    if (row_bytes % 16 != 0 || row_bytes > 512)
+    const int row_bytes = cache_row_bytes(D, dtype);
+    if (row_bytes == 0)
         return TSD_ERR_SHAPE;
     if (B == 0)
         return TSD_OK;
     if (!k_cache || !v_cache || !prefix_len || !out_path || !n_accepted || !new_prefix_len)
         return TSD_ERR_NULL;
-    if ((reinterpret_cast<uintptr_t>(k_cache) & 15u) || (reinterpret_cast<uintptr_t>(v_cache) & 15u))
+    if (!aligned16(k_cache) || !aligned16(v_cache))
         return TSD_ERR_ALIGN;
-    return tsd::launch_kv_commit(k_cache, v_cache, prefix_len, out_path, n_accepted, B, Tmax,
-                                 Hkv, Lmax, row_bytes, new_prefix_len, dev_status,
-                                 reinterpret_cast<cudaStream_t>(stream));
+    return tsd::launch_kv_commit(k_cache, v_cache, tsd::KvPages{}, prefix_len, out_path,
+                                 n_accepted, B, Tmax, Hkv, Lmax, row_bytes, new_prefix_len,
+                                 dev_status, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int tsd_kv_commit_paged(void *k_pages, void *v_pages, const int32_t *block_table, int num_pages,
+                        int page_size, int max_blocks, const int32_t *prefix_len,
+                        const int32_t *out_path, const int32_t *n_accepted, int B, int Tmax,
+                        int Hkv, int D, int dtype, int32_t *new_prefix_len, int32_t *dev_status,
+                        tsd_stream_t stream)
+{
+    TSD_NVTX_RANGE();
+    if (B < 0 || B > kMaxGridY || Tmax < 1 || Tmax > TSD_MAX_TREE || Hkv < 1 ||
+        !page_sizes_ok(num_pages, page_size, max_blocks))
+        return TSD_ERR_SHAPE;
+    if (dtype != TSD_F32 && dtype != TSD_BF16)
+        return TSD_ERR_DTYPE;
+    const int row_bytes = cache_row_bytes(D, dtype);
+    if (row_bytes == 0)
+        return TSD_ERR_SHAPE;
+    if (B == 0)
+        return TSD_OK;
+    if (!k_pages || !v_pages || !block_table || !prefix_len || !out_path || !n_accepted ||
+        !new_prefix_len)
+        return TSD_ERR_NULL;
+    if (!aligned16(k_pages) || !aligned16(v_pages))
+        return TSD_ERR_ALIGN;
+    return tsd::launch_kv_commit(
+        k_pages, v_pages, kv_pages(block_table, num_pages, page_size, max_blocks), prefix_len,
+        out_path, n_accepted, B, Tmax, Hkv, max_blocks * page_size, row_bytes, new_prefix_len,
+        dev_status, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int tsd_rope_append_paged(const void *q, int64_t q_batch, int64_t q_token, const void *k,
+                          int64_t k_batch, int64_t k_token, const void *v, int64_t v_batch,
+                          int64_t v_token, const double *inv_freq, int rot_dim, int interleaved,
+                          float rot_scale, const int32_t *prefix_len, const int32_t *n_new,
+                          const int32_t *depth, int B, int Tmax, int Hq, int Hkv, int D, int dtype,
+                          void *q_out, void *k_pages, void *v_pages, const int32_t *block_table,
+                          int num_pages, int page_size, int max_blocks, int32_t *dev_status,
+                          tsd_stream_t stream)
+{
+    TSD_NVTX_RANGE();
+    if (B < 0 || B > kMaxGridY || Tmax < 1 || Hq < 1 || Hkv < 1 || Hq > (1 << 20) ||
+        Hkv > (1 << 20) || !page_sizes_ok(num_pages, page_size, max_blocks))
+        return TSD_ERR_SHAPE;
+    if (dtype != TSD_F32 && dtype != TSD_BF16)
+        return TSD_ERR_DTYPE;
+    const int row_bytes = cache_row_bytes(D, dtype);
+    if (row_bytes == 0 || rot_dim < 2 || rot_dim > D || (rot_dim & 1))
+        return TSD_ERR_SHAPE;
+    const int es = dtype == TSD_F32 ? 4 : 2;
+    // rows of a token are dense; tokens and sequences may lie further apart
+    if (q_token < (int64_t)Hq * D || k_token < (int64_t)Hkv * D || v_token < (int64_t)Hkv * D ||
+        q_batch < 0 || k_batch < 0 || v_batch < 0)
+        return TSD_ERR_SHAPE;
+    if (B == 0)
+        return TSD_OK;
+    if (!q || !k || !v || !inv_freq || !prefix_len || !n_new || !q_out || !k_pages || !v_pages ||
+        !block_table)
+        return TSD_ERR_NULL;
+    for (const int64_t stride : {q_batch, q_token, k_batch, k_token, v_batch, v_token})
+        if (stride * es % 16 != 0)
+            return TSD_ERR_ALIGN;
+    for (const void *p : {q, k, v, (const void *)q_out, (const void *)k_pages,
+                          (const void *)v_pages})
+        if (!aligned16(p))
+            return TSD_ERR_ALIGN;
+    tsd::RopeArgs a;
+    a.q = q; a.k = k; a.v = v;
+    a.q_batch = q_batch; a.q_token = q_token; a.k_batch = k_batch; a.k_token = k_token;
+    a.v_batch = v_batch; a.v_token = v_token;
+    a.inv_freq = inv_freq; a.prefix_len = prefix_len; a.n_new = n_new; a.depth = depth;
+    a.Tmax = Tmax; a.Hq = Hq; a.Hkv = Hkv; a.D = D; a.rot = rot_dim; a.interleaved = interleaved;
+    a.rot_scale = rot_scale;
+    a.q_out = q_out; a.k_pages = k_pages; a.v_pages = v_pages; a.dev_status = dev_status;
+    a.pages = kv_pages(block_table, num_pages, page_size, max_blocks);
+    return tsd::launch_rope_append(a, B, dtype, device_sms(),
+                                   reinterpret_cast<cudaStream_t>(stream));
 }
 
 int tsd_tree_expand(const float *q_probs, int Rq, int V, const int32_t *frow, int k,

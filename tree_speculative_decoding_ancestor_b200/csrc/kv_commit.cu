@@ -23,13 +23,14 @@ namespace {
 constexpr int kCommitThreads = 256;
 
 __global__ void __launch_bounds__(kCommitThreads)
-    kv_commit_kernel(uint8_t *__restrict__ k, uint8_t *__restrict__ v,
+    kv_commit_kernel(uint8_t *__restrict__ k, uint8_t *__restrict__ v, KvPages pages,
                      const int32_t *__restrict__ prefix_len, const int32_t *__restrict__ out_path,
                      const int32_t *__restrict__ n_accepted, int Tmax, int Hkv, int Lmax,
                      int row_bytes, int32_t *__restrict__ new_prefix, int32_t *dev_status)
 {
     extern __shared__ uint4 stage[];   // [2 (K, V)][n][row_bytes / 16]
     __shared__ int s_path[kMaxTree];
+    __shared__ long long s_src[kMaxTree], s_dst[kMaxTree];   // cache rows of a move
     const int h = blockIdx.x, b = blockIdx.y;
     const int n = n_accepted[b], P = prefix_len[b];
     if (n < 0) {   // malformed upstream (already reported there): nothing moves
@@ -43,34 +44,43 @@ __global__ void __launch_bounds__(kCommitThreads)
     __syncthreads();
     if (ok && (int)threadIdx.x < n) {
         const int i = threadIdx.x, u = s_path[i];
-        ok = u >= 0 && u < Tmax && (i == 0 || u > s_path[i - 1]) && P + u < Lmax;
+        ok = u >= 0 && u < Tmax && (i == 0 || u > s_path[i - 1]) && u < Lmax - P;
     }
     ok = __syncthreads_and(ok) != 0;
+    bool bad_page = false;
+    if (ok && (int)threadIdx.x < n) {
+        const int i = threadIdx.x, u = s_path[i];
+        // rows in place need no page
+        s_src[i] = u == i ? 0 : kv_row(pages, b, h, Hkv, Lmax, P + u);
+        s_dst[i] = u == i ? 0 : kv_row(pages, b, h, Hkv, Lmax, P + i);
+        bad_page = s_src[i] < 0 || s_dst[i] < 0;
+    }
+    bad_page = __syncthreads_or(bad_page) != 0;
     if (h == 0 && threadIdx.x == 0) {
-        new_prefix[b] = ok ? P + n : P;
+        new_prefix[b] = ok && !bad_page ? P + n : P;
         if (!ok)
             flag(dev_status, TSD_DEV_BAD_PATH);
+        if (bad_page)
+            flag(dev_status, TSD_DEV_BAD_PAGE);
     }
-    if (!ok)
+    if (!ok || bad_page)
         return;
     const int vec = row_bytes / 16;
     const int total = n * vec;   // vectors per tensor
-    const size_t plane = (size_t)Lmax * row_bytes;
-    uint8_t *const kb = k + ((size_t)b * Hkv + h) * plane;
-    uint8_t *const vb = v + ((size_t)b * Hkv + h) * plane;
-    // extent of one (sequence, KV head) plane in 16-byte vectors
-    const long long plane_vec = (long long)Lmax * vec;
+    // extent of the cache in 16-byte vectors
+    const long long all_vec = kv_rows_total(pages, gridDim.y, Hkv, Lmax) * vec;
     for (int idx = threadIdx.x; idx < 2 * total; idx += kCommitThreads) {
         const int t = idx >= total, r = idx - t * total, i = r / vec, c = r - i * vec;
-        const int u = s_path[i];
-        if (u != i && in_bounds((long long)(P + u) * vec + c, plane_vec, dev_status))
-            stage[idx] = reinterpret_cast<const uint4 *>((t ? vb : kb) + (size_t)(P + u) * row_bytes)[c];
+        const long long at = s_src[i] * vec + c;
+        if (s_path[i] != i && in_bounds(at, all_vec, dev_status))
+            stage[idx] = reinterpret_cast<const uint4 *>(t ? v : k)[at];
     }
     __syncthreads();
     for (int idx = threadIdx.x; idx < 2 * total; idx += kCommitThreads) {
         const int t = idx >= total, r = idx - t * total, i = r / vec, c = r - i * vec;
-        if (s_path[i] != i && in_bounds((long long)(P + i) * vec + c, plane_vec, dev_status))
-            reinterpret_cast<uint4 *>((t ? vb : kb) + (size_t)(P + i) * row_bytes)[c] = stage[idx];
+        const long long at = s_dst[i] * vec + c;
+        if (s_path[i] != i && in_bounds(at, all_vec, dev_status))
+            reinterpret_cast<uint4 *>(t ? v : k)[at] = stage[idx];
     }
 }
 
@@ -78,10 +88,10 @@ size_t kv_commit_smem(int Tmax, int row_bytes) { return (size_t)2 * Tmax * row_b
 
 }  // namespace
 
-int launch_kv_commit(void *k_cache, void *v_cache, const int32_t *prefix_len,
-                     const int32_t *out_path, const int32_t *n_accepted, int B, int Tmax, int Hkv,
-                     int Lmax, int row_bytes, int32_t *new_prefix, int32_t *dev_status,
-                     cudaStream_t stream)
+int launch_kv_commit(void *k_cache, void *v_cache, const KvPages &pages,
+                     const int32_t *prefix_len, const int32_t *out_path,
+                     const int32_t *n_accepted, int B, int Tmax, int Hkv, int Lmax, int row_bytes,
+                     int32_t *new_prefix, int32_t *dev_status, cudaStream_t stream)
 {
     if (B == 0)
         return TSD_OK;
@@ -107,8 +117,8 @@ int launch_kv_commit(void *k_cache, void *v_cache, const int32_t *prefix_len,
         }
     }
     kv_commit_kernel<<<dim3(Hkv, B), kCommitThreads, smem, stream>>>(
-        static_cast<uint8_t *>(k_cache), static_cast<uint8_t *>(v_cache), prefix_len, out_path,
-        n_accepted, Tmax, Hkv, Lmax, row_bytes, new_prefix, dev_status);
+        static_cast<uint8_t *>(k_cache), static_cast<uint8_t *>(v_cache), pages, prefix_len,
+        out_path, n_accepted, Tmax, Hkv, Lmax, row_bytes, new_prefix, dev_status);
     TSD_LAUNCH_CHECK();
     return TSD_OK;
 }

@@ -187,10 +187,25 @@ int launch_tree_merge(const int32_t *ctok, const int32_t *cq, const int32_t *cle
                       int32_t *n_nodes, int32_t *dev_status, cudaStream_t stream);
 int launch_wait_probe(int kind, unsigned long long limit_ns, void *scratch,
                       int32_t *dev_status, cudaStream_t stream);
-int launch_kv_commit(void *k_cache, void *v_cache, const int32_t *prefix_len,
-                     const int32_t *out_path, const int32_t *n_accepted, int B, int Tmax, int Hkv,
-                     int Lmax, int row_bytes, int32_t *new_prefix, int32_t *dev_status,
-                     cudaStream_t stream);
+// Contiguous caches [B][Hkv][Lmax] rows, or (pages.table set) paged pools.
+int launch_kv_commit(void *k_cache, void *v_cache, const KvPages &pages,
+                     const int32_t *prefix_len, const int32_t *out_path,
+                     const int32_t *n_accepted, int B, int Tmax, int Hkv, int Lmax, int row_bytes,
+                     int32_t *new_prefix, int32_t *dev_status, cudaStream_t stream);
+
+struct RopeArgs {
+    const void *q, *k, *v;
+    // elements from one sequence, and from one token, to the next
+    long long q_batch, q_token, k_batch, k_token, v_batch, v_token;
+    const double *inv_freq;
+    const int32_t *prefix_len, *n_new, *depth;   // depth: nullptr for a chunk
+    int Tmax, Hq, Hkv, D, rot, interleaved;
+    float rot_scale;
+    void *q_out, *k_pages, *v_pages;
+    int32_t *dev_status;
+    KvPages pages;
+};
+int launch_rope_append(const RopeArgs &a, int B, int dtype, int num_sms, cudaStream_t stream);
 // true: greedy verification takes the all-rows scan for these sizes (else
 // the walk over matched nodes); reads TSD_GREEDY_FORM.
 bool greedy_all_rows(int B, int Tmax, int V);
