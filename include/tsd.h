@@ -72,6 +72,7 @@ enum tsd_dev_status {
     TSD_DEV_TIMEOUT = 16,     /* a bounded pipeline wait expired (kernel bailed out) */
     TSD_DEV_BAD_PATH = 32,    /* an accepted path that is not a valid commit list     */
     TSD_DEV_BAD_PAGE = 64,    /* a block-table entry outside [0, num_pages)          */
+    TSD_DEV_BAD_ROW = 256,    /* a sampling row without a candidate, or with bad settings   */
     TSD_DEV_BOUNDS = 128      /* checked build only (libtsd_checked.so): a kernel computed
                                  an index outside the buffer its arguments describe; the
                                  access was skipped                                    */
@@ -455,6 +456,40 @@ int tsd_rope_append_paged(const void *q, int64_t q_batch, int64_t q_token, const
                           void *q_out, void *k_pages, void *v_pages, const int32_t *block_table,
                           int num_pages, int page_size, int max_blocks, int32_t *dev_status,
                           tsd_stream_t stream);
+
+/*
+ * Sampling with temperature, top-k, top-p and min-p from given uniforms (the
+ * draft side of "ツリー検証アルゴリズム": its tokens are drawn from a
+ * distribution q that tsd_tree_verify_stochastic then needs as a q_probs
+ * row).  For every row r < R, with l its logits, T its temperature and
+ * w_i = exp((l_i - max l) / T), the kept set is
+ *   - the top_k largest entries (all, if top_k <= 0 or >= V),
+ *   - of these, in descending order, each entry in front of which lies less
+ *     than top_p of their sum (all, if top_p >= 1; always the first),
+ *   - of these, the entries with w_i >= min_p (min_p at most 1 counts);
+ * equal logits are ordered by token id, lowest first.  p = w over the kept
+ * set, normalised; tokens[r][s] is the smallest kept i whose ascending
+ * cumulative sum of p exceeds u[r][s].  T = 0 keeps the largest logit alone.
+ * NaN logits count as -inf; if +inf occurs, only +inf entries have weight.
+ *   logits       [R][V], dtype TSD_F32 or TSD_BF16, rows logits_ld elements
+ *                apart
+ *   temperature, top_p, min_p [R] fp32, top_k [R] int32; NULL: T = 1, off
+ *   u            [R][S] fp64 in [0, 1)
+ *   tokens       [R][S] int32, out
+ *   probs        [R][V] fp32, out, rows probs_ld elements apart (so that a
+ *                row can be a row of q_probs [B][Rq][V]); NULL: not wanted
+ * Weights are integers w_i = round(2^s exp(..)), s = min(50, 63 - log2 V
+ * rounded up), and all sums of them are exact: results do not depend on the
+ * launch.  Weights below 2^-s / 2 are 0 (never drawn).  A row whose logits
+ * are all -inf or NaN, whose temperature is not in [0, 1e30] or whose top_p
+ * or min_p is NaN sets TSD_DEV_BAD_ROW and gets tokens -1 and probs 0.
+ * V is at most 360448.  Host errors: TSD_ERR_NULL, TSD_ERR_SHAPE,
+ * TSD_ERR_DTYPE, TSD_ERR_CUDA.
+ */
+int tsd_sample(const void *logits, int64_t logits_ld, int dtype, int R, int V,
+               const float *temperature, const int32_t *top_k, const float *top_p,
+               const float *min_p, const double *u, int S, int32_t *tokens, float *probs,
+               int64_t probs_ld, int32_t *dev_status, tsd_stream_t stream);
 
 /*
  * Self-test of the bounded waits (no counterpart in the paper).  Every wait

@@ -81,8 +81,40 @@ def test_commit_arguments(lib):  # noqa: F811
     assert len(lib.calls) == n
 
 
+def _sample(R=3, V=50, S=2, **kw):
+    a = dict(logits=torch.zeros(R, V), u=torch.zeros(R, S, dtype=torch.float64))
+    a.update(kw)
+    return tsd.sample(**a)
+
+
+def test_sample_arguments(lib):  # noqa: F811
+    r = _sample()
+    assert r.tokens.shape == (3, 2) and r.probs is None
+    assert _sample(with_probs=True).probs.shape == (3, 50)
+    q = torch.zeros(3, 4, 50)
+    assert _sample(probs=q[:, 1]).probs.data_ptr() == q[:, 1].data_ptr()   # a row of q_probs
+    _sample(logits=torch.zeros(3, 64, **bf)[:, :50], temperature=torch.ones(3),
+            top_k=torch.ones(3, **i32), top_p=torch.ones(3), min_p=torch.ones(3))
+    n = len(lib.calls)
+    for bad in (dict(u=torch.zeros(2, 2, dtype=torch.float64)), dict(temperature=torch.ones(2)),
+                dict(logits=torch.zeros(50, 3).t()), dict(probs=torch.zeros(3, 49)),
+                dict(probs=torch.zeros(1, 50).expand(3, 50)), dict(logits=torch.zeros(50)),
+                dict(tokens=torch.zeros(3, 3, **i32))):
+        with pytest.raises(ValueError):
+            _sample(**bad)
+    for bad in (dict(u=torch.zeros(3, 2)), dict(top_k=torch.ones(3)), dict(top_p=torch.ones(3, **bf)),
+                dict(logits=torch.zeros(3, 50, dtype=torch.float16)), dict(probs=torch.zeros(3, 50, **bf)),
+                dict(temperature=1.0)):
+        with pytest.raises(TypeError):
+            _sample(**bad)
+    x = torch.zeros(3, 50)
+    with pytest.raises(ValueError, match="overlap"):
+        _sample(logits=x, probs=x)
+    assert len(lib.calls) == n
+
+
 def test_host_tensors_are_refused():
-    for call in (_rope, _commit):
+    for call in (_rope, _commit, _sample):
         with pytest.raises(ValueError, match="CUDA device"):
             call()
 
@@ -120,6 +152,22 @@ def test_c_entry_points_refuse():
         assert commit(**bad) == SHAPE
     assert commit(dt=7) == DTYPE
     assert commit(k=_U) == ALIGN
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="fake addresses must not reach a GPU")
+def test_c_sample_refuses():
+    L = tsd.load_library()
+
+    def sample(logits=_A, ld=100, dt=0, R=2, V=100, u=_A, S=1, tokens=_A, probs=_A, pld=100):
+        return L.tsd_sample(logits, ld, dt, R, V, None, None, None, None, u, S, tokens, probs, pld,
+                            None, None)
+    assert sample(R=0) == 0 and sample(S=0, probs=None) == 0
+    for bad in (dict(logits=None), dict(u=None), dict(tokens=None)):
+        assert sample(**bad) == -1
+    for bad in (dict(R=-1), dict(V=0), dict(ld=99), dict(pld=99), dict(S=-1), dict(S=1 << 20),
+                dict(V=360449, ld=360449, pld=360449)):
+        assert sample(**bad) == -2
+    assert sample(dt=2) == -3
 
 
 def test_rope_frequencies():

@@ -18,6 +18,7 @@ Six operations, each a thin wrapper over the C ABI of ``lib/libtsd.so``
 from .binding import (  # noqa: F401
     LIB_PATH,
     RopeFrequencies,
+    SampleResult,
     TsdError,
     Tree,
     TreeMask,
@@ -32,6 +33,7 @@ from .binding import (  # noqa: F401
     load_library,
     rope_append_paged,
     rope_frequencies,
+    sample,
     tree_attention,
     tree_attention_paged,
     tree_dfs_order,

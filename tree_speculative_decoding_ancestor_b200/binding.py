@@ -28,7 +28,7 @@ TSD_F32, TSD_BF16 = 0, 1
 TSD_MAX_TREE = 128
 TSD_TREE_INVALID = -2
 DEV_BAD_TREE, DEV_BAD_TOKEN, DEV_BAD_QROW, DEV_BAD_PREFIX, DEV_TIMEOUT = 1, 2, 4, 8, 16
-DEV_BAD_PATH, DEV_BAD_PAGE, DEV_BOUNDS = 32, 64, 128
+DEV_BAD_PATH, DEV_BAD_PAGE, DEV_BOUNDS, DEV_BAD_ROW = 32, 64, 128, 256
 
 _lock = threading.Lock()
 _lib: Optional[ctypes.CDLL] = None
@@ -68,6 +68,7 @@ _SIGNATURES: Dict[str, Tuple[object, list]] = {
     "tsd_rope_append_paged": (_I, [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I, _I,
                                    ctypes.c_float, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P,
                                    _P, _I, _I, _I, _P, _P]),
+    "tsd_sample": (_I, [_P, _I64, _I, _I, _I, _P, _P, _P, _P, _P, _I, _P, _P, _I64, _P, _P]),
     "tsd_debug_wait_probe": (_I, [_I, ctypes.c_ulonglong, _P, _P, _P]),
 }
 
@@ -113,7 +114,8 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _stream(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    # the handle itself: building a Stream object costs a microsecond a call
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _cuda(device: torch.device) -> None:
@@ -125,6 +127,9 @@ def _cuda(device: torch.device) -> None:
 
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape: Tuple[int, ...],
           device: torch.device) -> None:
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and \
+            t.device == device and t.is_contiguous():
+        return   # the common case at the cost of one pass over the attributes
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != device:
@@ -137,19 +142,33 @@ def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape: Tuple[int, ...]
         raise ValueError(f"{name} must be contiguous")
 
 
+_HERE_ALREADY = contextlib.nullcontext()
+
+
 def _on(device: torch.device):
-    """The library launches on the current device: make it the tensors' own."""
-    return torch.cuda.device(device) if device.type == "cuda" else contextlib.nullcontext()
+    """The library launches on the current device: make it the tensors' own
+    (entering a device costs microseconds, so only where it is another)."""
+    if device.type != "cuda" or torch.cuda.current_device() == device.index:
+        return _HERE_ALREADY
+    return torch.cuda.device(device)
+
+
+def _end(t: torch.Tensor) -> int:
+    """The address behind the last element of a non-empty tensor."""
+    if t.is_contiguous():
+        span = t.numel()
+    else:
+        span = 1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+    return t.data_ptr() + span * t.element_size()
 
 
 def _apart(out: torch.Tensor, name: str, *inputs: torch.Tensor) -> None:
-    """Refuse a dense output that shares memory with an input."""
-    lo, hi = out.data_ptr(), out.data_ptr() + out.numel() * out.element_size()
+    """Refuse an output whose memory range meets an input's."""
+    if not out.numel():
+        return
+    lo, hi = out.data_ptr(), _end(out)
     for t in inputs:
-        if not t.numel() or lo == hi:
-            continue
-        span = 1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
-        if t.data_ptr() < hi and lo < t.data_ptr() + span * t.element_size():
+        if t.data_ptr() < hi and t.numel() and lo < _end(t):
             raise ValueError(f"{name} must not overlap an input")
 
 
@@ -686,6 +705,72 @@ def tree_attention_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.
                                       _ptr(out), _ptr(ws), ws.numel(), _ptr(st), _stream(dev))
     _check(rc, "tsd_tree_attention_paged")
     return out
+
+
+class SampleResult(NamedTuple):
+    tokens: torch.Tensor              # [R][S] int32
+    probs: Optional[torch.Tensor]     # [R][V] float32: what the tokens were drawn from
+
+
+def _need_matrix(t: torch.Tensor, name: str, dtype: torch.dtype, shape: Tuple[int, int],
+                 device: torch.device) -> int:
+    """As _need, but only each row must be dense; returns the row step."""
+    if isinstance(t, torch.Tensor) and t.shape == shape and t.dim() == 2 and not t.is_contiguous():
+        if (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+            raise ValueError(f"{name}: rows must be contiguous and apart")
+        _need(t[:0], name, dtype, (0, shape[1]), device)
+        return t.stride(0)
+    _need(t, name, dtype, shape, device)
+    return shape[1]
+
+
+def sample(logits: torch.Tensor, u: torch.Tensor, temperature: Optional[torch.Tensor] = None,
+           top_k: Optional[torch.Tensor] = None, top_p: Optional[torch.Tensor] = None,
+           min_p: Optional[torch.Tensor] = None, tokens: Optional[torch.Tensor] = None,
+           probs: Optional[torch.Tensor] = None, with_probs: bool = False,
+           status: Optional[torch.Tensor] = None) -> SampleResult:
+    """Draw tokens from logits [R][V] (float32 or bfloat16, rows possibly
+    apart) with given uniforms u [R][S] float64: temperature, then top_k, then
+    top_p of what is left, then min_p against the maximum, each an [R] tensor
+    (float32; top_k int32) or None.  With `with_probs` or `probs` ([R][V]
+    float32, rows possibly apart: a slice of q_probs) the distribution the
+    tokens were drawn from comes too."""
+    lib = load_library()
+    dev = logits.device
+    _cuda(dev)
+    if logits.dim() != 2 or u.dim() != 2:
+        raise ValueError("logits must be [R][V] and u [R][S]")
+    R, V = logits.shape
+    S = u.shape[1]
+    dt = {torch.float32: TSD_F32, torch.bfloat16: TSD_BF16}.get(logits.dtype)
+    if dt is None:
+        raise TypeError("logits must be float32 or bfloat16")
+    ld = _need_matrix(logits, "logits", logits.dtype, (R, V), dev)
+    _need(u, "u", torch.float64, (R, S), dev)
+    if temperature is not None:
+        _need(temperature, "temperature", torch.float32, (R,), dev)
+    if top_k is not None:
+        _need(top_k, "top_k", torch.int32, (R,), dev)
+    if top_p is not None:
+        _need(top_p, "top_p", torch.float32, (R,), dev)
+    if min_p is not None:
+        _need(min_p, "min_p", torch.float32, (R,), dev)
+    if tokens is None:
+        tokens = torch.empty((R, S), dtype=torch.int32, device=dev)
+    _need(tokens, "tokens", torch.int32, (R, S), dev)
+    if probs is None and with_probs:
+        probs = torch.empty((R, V), dtype=torch.float32, device=dev)
+    probs_ld = 0
+    if probs is not None:
+        probs_ld = _need_matrix(probs, "probs", torch.float32, (R, V), dev)
+        _apart(probs, "probs", logits)
+    st = _status_for(dev, status)
+    with _on(dev):
+        rc = lib.tsd_sample(_ptr(logits), ld, dt, R, V, _ptr(temperature), _ptr(top_k),
+                            _ptr(top_p), _ptr(min_p), _ptr(u), S, _ptr(tokens), _ptr(probs),
+                            probs_ld, _ptr(st), _stream(dev))
+    _check(rc, "tsd_sample")
+    return SampleResult(tokens, probs)
 
 
 class Tree(NamedTuple):

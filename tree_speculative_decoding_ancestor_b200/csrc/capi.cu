@@ -396,6 +396,29 @@ int tsd_rope_append_paged(const void *q, int64_t q_batch, int64_t q_token, const
                                    reinterpret_cast<cudaStream_t>(stream));
 }
 
+int tsd_sample(const void *logits, int64_t logits_ld, int dtype, int R, int V,
+               const float *temperature, const int32_t *top_k, const float *top_p,
+               const float *min_p, const double *u, int S, int32_t *tokens, float *probs,
+               int64_t probs_ld, int32_t *dev_status, tsd_stream_t stream)
+{
+    TSD_NVTX_RANGE();
+    if (R < 0 || R > (1 << 24) || V < 1 || V > tsd::sample_max_vocab() || S < 0 || S > 65536 ||
+        logits_ld < V || (probs && probs_ld < V))
+        return TSD_ERR_SHAPE;
+    if (dtype != TSD_F32 && dtype != TSD_BF16)
+        return TSD_ERR_DTYPE;
+    if (R == 0 || (S == 0 && !probs))
+        return TSD_OK;
+    if (!logits || (S > 0 && (!u || !tokens)))
+        return TSD_ERR_NULL;
+    tsd::SampleArgs a;
+    a.logits = logits; a.ld = logits_ld; a.V = V; a.S = S;
+    a.temperature = temperature; a.top_k = top_k; a.top_p = top_p; a.min_p = min_p;
+    a.u = u; a.tokens = tokens; a.probs = probs; a.probs_ld = probs_ld;
+    a.dev_status = dev_status;
+    return tsd::launch_sample(a, R, dtype, device_sms(), reinterpret_cast<cudaStream_t>(stream));
+}
+
 int tsd_tree_expand(const float *q_probs, int Rq, int V, const int32_t *frow, int k,
                     int32_t *parent, int32_t *tokens, int32_t *q_row, int32_t *n_nodes,
                     int32_t *lvl_begin, int B, int Tmax, int32_t *dev_status,

@@ -1,0 +1,554 @@
+// Tokens from filtered logits and given uniforms.
+//
+// One row of logits l, temperature T: w_i = exp((l_i - max l) / T).  The kept
+// set is the top_k largest entries, of these the smallest prefix (in
+// descending order) that holds top_p of their sum, of these the entries with
+// w_i >= min_p; equal logits are ordered by token id.  p is w over the kept
+// set's sum, and draw s is the smallest kept i whose ascending cumulative sum
+// of p exceeds u_s.
+//
+// Weights are held as integers, w_i = round(2^s exp(..)) with V 2^s <= 2^63:
+// every sum is exact, so its value does not depend on the order in which the
+// threads and atomics add, and the thresholds and draws of two runs are equal
+// by construction.  The exponentials are fp64 (fp32 ones would move a CDF
+// by 1e-7 and with it one draw in some thousands); the rounding to 2^-s
+// (s = 46 at V = 128256) moves it by about 1e-11.
+//
+// A row belongs to a cluster of C CTAs; each loads its chunk of the row once
+// into shared memory, and every later pass reads it there.
+//   1  max and min of the row
+//   2  (top_k or top_p) a histogram over 1024 equal steps of the logit: count
+//      and mass per step, added up over the cluster; a scan finds the step in
+//      which the k-th entry, or the top_p mass, falls
+//   3  that step's entries (usually tens) are gathered, and every entry sums
+//      the count and mass in front of it; the one at which the limit is
+//      passed is the threshold, as a 64-bit (logit, token id) key.  More than
+//      kList entries: the same histogram over the keys' range inside the
+//      step, ten bits of the key a round, until few are left -- keys are
+//      distinct, so this ends also when all logits are equal
+//   4  the kept sums of each warp's segment, from them each draw's segment,
+//      which its warp walks; the probabilities
+// Bound: the read of the logits and the write of the probabilities; the
+// exponentials of step 2 (about 20 fp64-pipe slots an entry) come close.
+#include <algorithm>
+#include <atomic>
+
+#include "cluster_xchg.cuh"
+#include "fp64_exp.cuh"
+#include "tsd_common.cuh"
+
+namespace tsd {
+
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kBins = 2 * kThreads;     // steps of a histogram
+constexpr int kList = 1024;             // entries gathered at most
+constexpr int kMaxCluster = 8;
+constexpr int kMaxChunk = 45056;        // logits of a CTA: 176 KB of shared memory
+constexpr float kReach = 40.f;          // e^-40 2^s < 1/2: weights from there on are 0
+
+typedef unsigned long long u64;
+
+struct Shared {
+    double table[kExpTable];
+    u64 mass[kBins];
+    uint32_t count[kBins];
+    u64 key[kList], weight[kList];      // gathered entries of this CTA
+    u64 all_key[kList], all_weight[kList];
+    u64 warp_sum[kWarps];
+    u64 scan_mass[kWarps];
+    uint32_t scan_count[kWarps];
+    float hi, lo;                       // the CTA's largest and smallest logit
+    u64 key_hi, key_lo;                 // of the entries in question
+    uint32_t listed;
+    // the step (or entry) a search ended at
+    u64 found_mass, found_before_mass, found_key;
+    uint32_t found_bin, found_count, found_before;
+};
+
+__device__ __forceinline__ u64 remote_u64(const void *p, uint32_t rank)
+{
+    u64 v;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];"
+                 : "=l"(v)
+                 : "r"(cluster_map(xchg_smem_addr(p), rank))
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint32_t remote_u32(const void *p, uint32_t rank)
+{
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];"
+                 : "=r"(v)
+                 : "r"(cluster_map(xchg_smem_addr(p), rank))
+                 : "memory");
+    return v;
+}
+
+// Larger logit first, then lower token id: descending order of this key.
+__device__ __forceinline__ u64 order_key(float l, uint32_t token)
+{
+    uint32_t u = __float_as_uint(l);
+    u ^= (u >> 31) ? 0xffffffffu : 0x80000000u;
+    return ((u64)u << 32) | (0xffffffffu - token);
+}
+
+struct Row {
+    const float *l;       // this CTA's logits (shared memory)
+    int n, first;         // how many, and the token id of the first
+    int C, rank;
+    float top;            // the row's largest logit
+    double inv_t;
+    float step;           // histogram steps per logit unit
+
+    __device__ __forceinline__ u64 weight(float x, const double *table) const
+    {
+        const double d = x == top ? 0.0 : ((double)x - (double)top) * inv_t;   // inf - inf
+        return __double2ull_rn(table_exp(d, table));
+    }
+    __device__ __forceinline__ int bin(float x) const   // kBins: out of reach, weight 0
+    {
+        const float f = x == top ? 0.f : (top - x) * step;
+        return f < (float)kBins ? (int)f : kBins;
+    }
+};
+
+// The histogram of every CTA added up: thread t has steps 2t and 2t + 1 with
+// what lies in front of each.
+struct Scan {
+    u64 mass[2], before_mass[2];
+    uint32_t count[2], before[2];
+};
+
+__device__ __forceinline__ void combine_and_scan(Shared &sh, int C, Scan &sc)
+{
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    cluster_sync_all();   // the histograms are complete
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        sc.mass[i] = 0;
+        sc.count[i] = 0;
+        for (int r = 0; r < C; ++r) {
+            sc.mass[i] += remote_u64(&sh.mass[2 * t + i], r);
+            sc.count[i] += remote_u32(&sh.count[2 * t + i], r);
+        }
+    }
+    u64 m = sc.mass[0] + sc.mass[1];
+    uint32_t c = sc.count[0] + sc.count[1];
+    const u64 own_m = m;
+    const uint32_t own_c = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const u64 pm = __shfl_up_sync(0xffffffffu, m, o);
+        const uint32_t pc = __shfl_up_sync(0xffffffffu, c, o);
+        if (lane >= o) {
+            m += pm;
+            c += pc;
+        }
+    }
+    if (lane == 31) {
+        sh.scan_mass[warp] = m;
+        sh.scan_count[warp] = c;
+    }
+    __syncthreads();
+    m -= own_m;
+    c -= own_c;
+    for (int w = 0; w < warp; ++w) {
+        m += sh.scan_mass[w];
+        c += sh.scan_count[w];
+    }
+    sc.before_mass[0] = m;
+    sc.before[0] = c;
+    sc.before_mass[1] = m + sc.mass[0];
+    sc.before[1] = c + sc.count[0];
+    cluster_sync_all();   // every CTA has read the histograms: they may be reused
+}
+
+// Where the limit (an entry count, or a mass) falls; sh.found_* for all.
+// Some step holds it: 0 < limit <= the total.
+__device__ __forceinline__ void find_step(Shared &sh, const Scan &sc, bool by_mass, u64 limit)
+{
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const bool here = by_mass ? sc.before_mass[i] < limit &&
+                                        limit <= sc.before_mass[i] + sc.mass[i]
+                                  : sc.before[i] < limit && limit <= sc.before[i] + sc.count[i];
+        if (here) {
+            sh.found_bin = 2 * threadIdx.x + i;
+            sh.found_before = sc.before[i];
+            sh.found_before_mass = sc.before_mass[i];
+            sh.found_count = sc.count[i];
+            sh.found_mass = sc.mass[i];
+        }
+    }
+    __syncthreads();
+}
+
+// The entry of step `bin` (found_count entries behind found_before and
+// found_before_mass) at which the limit is passed.  Returns its key, and in
+// mass_incl the mass up to and including it.
+__device__ u64 resolve(Shared &sh, const Row &row, int bin, bool by_mass, u64 limit, u64 *mass_incl)
+{
+    u64 lo = 0, hi = ~0ull;   // keys in question
+    uint32_t count = sh.found_count, before = sh.found_before;
+    u64 before_mass = sh.found_before_mass;
+    __syncthreads();
+    while (count > (uint32_t)kList) {
+        if (threadIdx.x == 0) {
+            sh.key_hi = 0;
+            sh.key_lo = ~0ull;
+        }
+        __syncthreads();
+        u64 khi = 0, klo = ~0ull;
+        for (int i = threadIdx.x; i < row.n; i += kThreads) {
+            const float x = row.l[i];
+            if (row.bin(x) != bin)
+                continue;
+            const u64 k = order_key(x, row.first + i);
+            if (k < lo || k > hi)
+                continue;
+            khi = max(khi, k);
+            klo = min(klo, k);
+        }
+        atomicMax(&sh.key_hi, khi);
+        atomicMin(&sh.key_lo, klo);
+        for (int i = threadIdx.x; i < kBins; i += kThreads) {
+            sh.mass[i] = 0;
+            sh.count[i] = 0;
+        }
+        cluster_sync_all();
+        for (int r = 0; r < row.C; ++r) {
+            khi = max(khi, remote_u64(&sh.key_hi, r));
+            klo = min(klo, remote_u64(&sh.key_lo, r));
+        }
+        hi = khi;
+        lo = klo;
+        const int shift = max(0, 64 - __clzll((long long)(hi - lo)) - 10);   // 1024 steps
+        for (int i = threadIdx.x; i < row.n; i += kThreads) {
+            const float x = row.l[i];
+            if (row.bin(x) != bin)
+                continue;
+            const u64 k = order_key(x, row.first + i);
+            if (k < lo || k > hi)
+                continue;
+            const int s = (int)((hi - k) >> shift);
+            atomicAdd(&sh.count[s], 1u);
+            atomicAdd(&sh.mass[s], row.weight(x, sh.table));
+        }
+        Scan sc;
+        combine_and_scan(sh, row.C, sc);
+        find_step(sh, sc, by_mass, by_mass ? limit - before_mass : limit - before);
+        hi -= (u64)sh.found_bin << shift;
+        lo = max(lo, hi - (((u64)1 << shift) - 1));
+        count = sh.found_count;
+        before += sh.found_before;
+        before_mass += sh.found_before_mass;
+        __syncthreads();
+    }
+    if (threadIdx.x == 0)
+        sh.listed = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < row.n; i += kThreads) {
+        const float x = row.l[i];
+        if (row.bin(x) != bin)
+            continue;
+        const u64 k = order_key(x, row.first + i);
+        if (k < lo || k > hi)
+            continue;
+        const uint32_t at = atomicAdd(&sh.listed, 1u);
+        sh.key[at] = k;
+        sh.weight[at] = row.weight(x, sh.table);
+    }
+    cluster_sync_all();
+    int n = 0;
+    for (int r = 0; r < row.C; ++r) {
+        const int m = (int)remote_u32(&sh.listed, r);
+        for (int i = threadIdx.x; i < m; i += kThreads) {
+            sh.all_key[n + i] = remote_u64(&sh.key[i], r);
+            sh.all_weight[n + i] = remote_u64(&sh.weight[i], r);
+        }
+        n += m;
+    }
+    cluster_sync_all();   // lists read everywhere (and all_* complete here)
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        const u64 k = sh.all_key[i], w = sh.all_weight[i];
+        u64 m = before_mass;
+        uint32_t c = before;
+        for (int j = 0; j < n; ++j) {
+            const bool ahead = sh.all_key[j] > k;
+            c += ahead ? 1u : 0u;
+            m += ahead ? sh.all_weight[j] : 0ull;
+        }
+        if (by_mass ? m < limit && limit <= m + w : c + 1 == limit) {
+            sh.found_key = k;
+            sh.found_mass = m + w;
+        }
+    }
+    __syncthreads();
+    *mass_incl = sh.found_mass;
+    return sh.found_key;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+    sample_kernel(SampleArgs a, int C, int chunk, double scale)
+{
+    extern __shared__ uint8_t smem_raw[];
+    Shared &sh = *reinterpret_cast<Shared *>(smem_raw);
+    float *l = reinterpret_cast<float *>(smem_raw + sizeof(Shared));
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    Row row;
+    row.C = C;
+    row.rank = (int)cluster_ctarank();
+    const long long r = blockIdx.x / C;
+    row.l = l;
+    row.first = row.rank * chunk;
+    row.n = max(0, min(chunk, a.V - row.first));
+
+    // 1: the chunk into shared memory; NaN counts as -inf, -0 as +0
+    const T *src = static_cast<const T *>(a.logits) + r * a.ld + row.first;
+    float hi = -INFINITY, lo = INFINITY;
+    auto put = [&](int i, float x) {
+        x = x != x ? -INFINITY : x + 0.f;
+        l[i] = x;
+        hi = fmaxf(hi, x);
+        lo = x > -INFINITY ? fminf(lo, x) : lo;
+    };
+    constexpr int N = 16 / sizeof(T);
+    int done = 0;
+    if ((reinterpret_cast<uintptr_t>(src) & 15u) == 0) {   // whole 16-byte vectors
+        const int nv = row.n / N;
+#pragma unroll 4
+        for (int i = t; i < nv; i += kThreads) {
+            union {
+                uint4 raw;
+                T e[N];
+            } x;
+            x.raw = __ldg(reinterpret_cast<const uint4 *>(src) + i);
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                put(i * N + j, to_float(x.e[j]));
+        }
+        done = nv * N;
+    }
+    for (int i = done + t; i < row.n; i += kThreads)
+        put(i, to_float(src[i]));
+    fill_exp_table(sh.table, scale);
+    for (int i = t; i < kBins; i += kThreads) {
+        sh.mass[i] = 0;
+        sh.count[i] = 0;
+    }
+    hi = warp_max(hi);
+    lo = -warp_max(-lo);
+    if (lane == 0) {
+        sh.scan_mass[warp] = ((u64)__float_as_uint(hi) << 32) | __float_as_uint(lo);
+    }
+    __syncthreads();
+    if (t == 0) {
+        for (int w = 0; w < kWarps; ++w) {
+            hi = fmaxf(hi, __uint_as_float((uint32_t)(sh.scan_mass[w] >> 32)));
+            lo = fminf(lo, __uint_as_float((uint32_t)sh.scan_mass[w]));
+        }
+        sh.hi = hi;
+        sh.lo = lo;
+    }
+    cluster_sync_all();
+    for (int q = 0; q < C; ++q) {
+        hi = fmaxf(hi, __uint_as_float(remote_u32(&sh.hi, q)));
+        lo = fminf(lo, __uint_as_float(remote_u32(&sh.lo, q)));
+    }
+    row.top = hi;
+
+    float T_ = a.temperature ? a.temperature[r] : 1.f;
+    int top_k = a.top_k ? a.top_k[r] : 0;
+    float top_p = a.top_p ? a.top_p[r] : 1.f;
+    float min_p = a.min_p ? a.min_p[r] : 0.f;
+    const bool bad = !(hi > -INFINITY) || !(T_ >= 0.f && T_ <= 1e30f) || top_p != top_p ||
+                     min_p != min_p;
+    if (T_ == 0.f) {   // the largest logit, lowest token id
+        T_ = 1.f;
+        top_k = 1;
+        top_p = 1.f;
+        min_p = 0.f;
+    }
+    float *probs = a.probs ? a.probs + r * a.probs_ld + row.first : nullptr;
+    if (bad) {   // the same on every CTA of the cluster
+        if (row.rank == 0) {
+            if (t == 0)
+                flag(a.dev_status, TSD_DEV_BAD_ROW);
+            for (int s = t; s < a.S; s += kThreads)
+                a.tokens[r * a.S + s] = -1;
+        }
+        for (int i = t; probs && i < row.n; i += kThreads)
+            probs[i] = 0.f;
+        cluster_sync_all();   // no CTA leaves while a peer reads its extremes
+        return;
+    }
+    row.inv_t = 1.0 / (double)T_;
+    row.step = (float)(kBins - 1) / fmaxf(fminf(hi - lo, kReach * T_), 1e-30f);
+
+    // 2, 3: the threshold
+    u64 threshold = 0;   // kept: keys from here up
+    if (top_k > 0 || top_p < 1.f) {
+        const bool with_mass = top_p < 1.f;
+        for (int i = t; i < row.n; i += kThreads) {
+            const float x = l[i];
+            const int b = row.bin(x);
+            if (b >= kBins)
+                continue;
+            atomicAdd(&sh.count[b], 1u);
+            if (with_mass)
+                atomicAdd(&sh.mass[b], row.weight(x, sh.table));
+        }
+        Scan sc;
+        combine_and_scan(sh, C, sc);
+        if (t == kThreads - 1) {
+            sh.found_count = sc.before[1] + sc.count[1];
+            sh.found_mass = sc.before_mass[1] + sc.mass[1];
+        }
+        __syncthreads();
+        u64 total = sh.found_mass;
+        const uint32_t entries = sh.found_count;
+        __syncthreads();
+        if (top_k > 0 && (uint32_t)top_k < entries) {
+            find_step(sh, sc, false, (u64)top_k);
+            threshold = resolve(sh, row, (int)sh.found_bin, false, (u64)top_k, &total);
+            __syncthreads();
+        }
+        if (with_mass) {
+            const u64 want = (u64)fmax(ceil((double)top_p * (double)total), 1.0);
+            const u64 limit = min(max(want, (u64)1), total);
+            find_step(sh, sc, true, limit);
+            u64 incl;
+            threshold = resolve(sh, row, (int)sh.found_bin, true, limit, &incl);
+            __syncthreads();
+        }
+    }
+
+    // 4: kept sums of the warps' segments (contiguous, in token order)
+    const u64 floor_w = (u64)ceil((double)fminf(fmaxf(min_p, 0.f), 1.f) * scale);
+    const int seg = (chunk + kWarps - 1) / kWarps;
+    const int s0 = min(warp * seg, row.n), s1 = min(s0 + seg, row.n);
+    auto kept = [&](int i) -> u64 {   // the weight of entry i, 0 if it is not kept
+        const float x = l[i];
+        if (order_key(x, row.first + i) < threshold || row.bin(x) >= kBins)
+            return 0;
+        const u64 w = row.weight(x, sh.table);
+        return w >= floor_w ? w : 0;
+    };
+    u64 sum = 0;
+    for (int i = s0 + lane; i < s1; i += 32)
+        sum += kept(i);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0)
+        sh.warp_sum[warp] = sum;
+    cluster_sync_all();
+    u64 total = 0, before = 0;   // of the row, and in front of this warp's segment
+    for (int i = lane; i < C * kWarps; i += 32) {
+        const u64 w = remote_u64(&sh.warp_sum[i % kWarps], i / kWarps);
+        total += w;
+        before += i < row.rank * kWarps + warp ? w : 0;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        total += __shfl_xor_sync(0xffffffffu, total, o);
+        before += __shfl_xor_sync(0xffffffffu, before, o);
+    }
+    for (int s = 0; s < a.S; ++s) {
+        const double x = a.u[r * a.S + s] * (double)total;
+        const u64 at = x > 0.0 ? min((u64)x, total - 1) : 0;   // first cumulative sum above it
+        if (at < before || at >= before + sum)
+            continue;
+        u64 run = before;
+        for (int i = s0; i < s1; i += 32) {
+            u64 c = i + lane < s1 ? kept(i + lane) : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const u64 p = __shfl_up_sync(0xffffffffu, c, o);
+                c += lane >= o ? p : 0;
+            }
+            const uint32_t over = __ballot_sync(0xffffffffu, run + c > at);
+            if (over) {
+                if (lane == 0)
+                    a.tokens[r * a.S + s] = row.first + i + __ffs(over) - 1;
+                break;
+            }
+            run += __shfl_sync(0xffffffffu, c, 31);
+        }
+    }
+    if (probs) {
+        const double inv = 1.0 / (double)total;
+        int from = 0;
+        if ((reinterpret_cast<uintptr_t>(probs) & 15u) == 0) {
+            const int nv = row.n / 4;
+            for (int i = t; i < nv; i += kThreads)
+                reinterpret_cast<float4 *>(probs)[i] =
+                    make_float4((float)((double)kept(4 * i) * inv), (float)((double)kept(4 * i + 1) * inv),
+                                (float)((double)kept(4 * i + 2) * inv),
+                                (float)((double)kept(4 * i + 3) * inv));
+            from = nv * 4;
+        }
+        for (int i = from + t; i < row.n; i += kThreads)
+            probs[i] = (float)((double)kept(i) * inv);
+    }
+    cluster_sync_all();   // no CTA leaves while a peer reads its sums
+}
+
+}  // namespace
+
+int sample_max_vocab() { return kMaxCluster * kMaxChunk; }
+
+int launch_sample(const SampleArgs &a, int R, int dtype, int num_sms, cudaStream_t stream)
+{
+    // CTAs per row: as few as hold the row in shared memory at two CTAs per
+    // SM; more (down to 4096 logits each) while the rows alone leave SMs idle.
+    int C = 1;
+    while (C < kMaxCluster && (a.V + C - 1) / C > 20480)
+        C *= 2;
+    while (C < kMaxCluster && (long long)R * C < num_sms && (a.V + C - 1) / C > 4096)
+        C *= 2;
+    int chunk = ((a.V + C - 1) / C + 7) & ~7;
+    int log2v = 0;
+    while ((1LL << log2v) < a.V)
+        ++log2v;
+    const int s = std::min(50, 63 - log2v);
+    const size_t smem = sizeof(Shared) + (size_t)chunk * sizeof(float);
+    auto kern = dtype == TSD_BF16 ? sample_kernel<__nv_bfloat16> : sample_kernel<float>;
+    constexpr int kMaxDevices = 64;
+    static std::atomic<bool> raised[kMaxDevices][2];
+    int dev = 0;
+    TSD_CUDA_TRY(cudaGetDevice(&dev));
+    if (dev < 0 || dev >= kMaxDevices)
+        return TSD_ERR_CUDA;
+    if (!raised[dev][dtype == TSD_BF16].load()) {
+        TSD_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                          (int)(sizeof(Shared) + kMaxChunk * sizeof(float))));
+        raised[dev][dtype == TSD_BF16].store(true);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((long long)R * C));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = C;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, kern, a, C, chunk, ldexp(1.0, s));
+    if (err != cudaSuccess) {
+        (void)cudaGetLastError();
+        return TSD_ERR_CUDA;
+    }
+    TSD_LAUNCH_CHECK();
+    return TSD_OK;
+}
+
+}  // namespace tsd

@@ -205,6 +205,22 @@ struct RopeArgs {
     int32_t *dev_status;
     KvPages pages;
 };
+
+struct SampleArgs {
+    const void *logits;
+    long long ld;                    // elements from one row to the next
+    int V, S;
+    const float *temperature;        // [R] each, nullptr: off
+    const int32_t *top_k;
+    const float *top_p, *min_p;
+    const double *u;                 // [R][S]
+    int32_t *tokens;                 // [R][S]
+    float *probs;                    // nullptr: not wanted
+    long long probs_ld;
+    int32_t *dev_status;
+};
+int sample_max_vocab();
+int launch_sample(const SampleArgs &a, int R, int dtype, int num_sms, cudaStream_t stream);
 int launch_rope_append(const RopeArgs &a, int B, int dtype, int num_sms, cudaStream_t stream);
 // true: greedy verification takes the all-rows scan for these sizes (else
 // the walk over matched nodes); reads TSD_GREEDY_FORM.
