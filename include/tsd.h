@@ -212,6 +212,44 @@ int tsd_tree_attention_paged(const void *q, const void *k_pages, const void *v_p
                              float scale, int dtype, void *out, void *workspace,
                              size_t workspace_bytes, int32_t *dev_status, tsd_stream_t stream);
 
+/*
+ * Causal attention of a chunk of new tokens over a paged KV cache: what
+ * brings a prompt into the cache (chunks of any length) or decodes one token
+ * per sequence (Tmax = 1), next to tree attention.  Sequence b has
+ * T_b = chunk_len[b] <= Tmax new tokens behind P_b = prefix_len[b] cached ones;
+ * their K and V rows are in the cache already (tsd_rope_append_paged):
+ *   out[b][t][h] = sum_{j <= P_b + t} softmax_j(scale * q[b][t][h] . k_j) v_j
+ * with k_j, v_j from KV head h / (Hq / Hkv).  A chunk of a tree's chain gives
+ * what tree attention gives.
+ *   q, out       [B][Tmax][Hq][D] dtype; rows t >= T_b are not written
+ *   k_pages, v_pages, block_table   as for tsd_tree_attention_paged
+ *   prefix_len, chunk_len [B] int32 (either may be 0)
+ *   workspace    tsd_chunk_attention_workspace_size() bytes; it depends on the
+ *                sizes and the current device only
+ * dtype TSD_BF16 (tensor cores; fp32 accumulation and softmax, probabilities
+ * rounded to bf16 for the product with V) or TSD_F32, D = 64 or 128,
+ * 0 < scale <= 1e30.  Keys at or beyond P_b + T_b never reach a result,
+ * whatever the cache holds there; the K and V rows in front of it are finite
+ * numbers (a V row that is not reaches also the tokens of its chunk in front
+ * of it, as 0 * inf does).  Pointers 16-byte aligned; B at most 65535,
+ * B * Hkv at most 2^24, Tmax * Hq / Hkv at most 2^30.
+ * Host errors: TSD_ERR_NULL, TSD_ERR_SHAPE, TSD_ERR_DTYPE, TSD_ERR_ALIGN,
+ * TSD_ERR_WORKSPACE, TSD_ERR_CUDA.  Device: TSD_DEV_BAD_PREFIX (T_b outside
+ * [0, Tmax] or P_b + T_b outside the table: that sequence's rows are not
+ * written), TSD_DEV_BAD_PAGE (a block-table entry outside [0, num_pages) for a
+ * key in use: it reads as page 0 or zero), TSD_DEV_TIMEOUT.
+ */
+int tsd_chunk_attention_paged(const void *q, const void *k_pages, const void *v_pages,
+                              const int32_t *block_table, int num_pages, int page_size,
+                              int max_blocks, const int32_t *prefix_len, const int32_t *chunk_len,
+                              int B, int Tmax, int Hq, int Hkv, int D, float scale, int dtype,
+                              void *out, void *workspace, size_t workspace_bytes,
+                              int32_t *dev_status, tsd_stream_t stream);
+
+/* Bytes of workspace tsd_chunk_attention_paged needs for these sizes (0: none). */
+size_t tsd_chunk_attention_workspace_size(int B, int Tmax, int Hq, int Hkv, int D, int page_size,
+                                          int max_blocks, int dtype);
+
 /* Bytes of workspace either verify call needs: a fixed ~40 KB (per-CTA
  * partial sums and barrier counters of the stochastic walk) plus 4 bytes per
  * logits row (greedy row argmax). */

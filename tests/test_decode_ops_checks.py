@@ -11,6 +11,7 @@ import pytest
 import torch
 
 import tree_speculative_decoding_ancestor_b200 as tsd
+from tree_speculative_decoding_ancestor_b200 import binding
 from test_binding_checks import lib  # noqa: F401  (fixture)
 
 i32 = dict(dtype=torch.int32)
@@ -113,8 +114,38 @@ def test_sample_arguments(lib):  # noqa: F811
     assert len(lib.calls) == n
 
 
+def _chunk(**kw):
+    a = dict(q=torch.zeros(B, T, Hq, D, **bf), prefix_len=torch.zeros(B, **i32),
+             chunk_len=torch.zeros(B, **i32), workspace=torch.empty(64, dtype=torch.uint8), **_cache())
+    a.update(kw)
+    return tsd.chunk_attention_paged(**a)
+
+
+def test_chunk_arguments(lib):  # noqa: F811
+    assert _chunk().shape == (B, T, Hq, D)
+    n = len(lib.calls)
+    q = torch.zeros(B, T, Hq, D, **bf)
+    for bad in (dict(q=q, out=q), dict(out=q[:, :T - 1]), dict(chunk_len=torch.zeros(B + 1, **i32)),
+                dict(q=torch.zeros(B, Hq, T, D, **bf).transpose(1, 2)),
+                dict(block_table=torch.zeros(B, **i32)), dict(q=q[0]),
+                dict(v_pages=torch.zeros(6, Hkv, page, 128, **bf))):
+        with pytest.raises(ValueError):
+            _chunk(**bad)
+    for bad in (dict(q=q.float()), dict(prefix_len=torch.zeros(B)), dict(workspace=torch.empty(64))):
+        with pytest.raises(TypeError):
+            _chunk(**bad)
+    assert all(c.endswith("workspace_size") for c in lib.calls[n:])
+
+
+def test_captured_calls_have_scratch_of_their_own(lib, monkeypatch):  # noqa: F811
+    monkeypatch.setattr(binding, "_workspace", {})
+    dev = torch.device("cpu")
+    assert binding._scratch_for(dev, "chunk", 0, None) is None
+    assert binding._scratch_for(dev, "chunk", 64, None) is binding._scratch_for(dev, "chunk", 64, None)
+
+
 def test_host_tensors_are_refused():
-    for call in (_rope, _commit, _sample):
+    for call in (_rope, _commit, _sample, _chunk):
         with pytest.raises(ValueError, match="CUDA device"):
             call()
 
@@ -168,6 +199,29 @@ def test_c_sample_refuses():
                 dict(V=360449, ld=360449, pld=360449)):
         assert sample(**bad) == -2
     assert sample(dt=2) == -3
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="fake addresses must not reach a GPU")
+def test_c_chunk_refuses():
+    L = tsd.load_library()
+
+    def chunk(q=_A, B=2, T=4, Hq=4, Hkv=2, D=64, dt=1, ps=16, blocks=2, pages=4, scale=0.1, ws=_A,
+              nbytes=1 << 30, table=_A):
+        return L.tsd_chunk_attention_paged(q, _A, _A, table, pages, ps, blocks, _A, _A, B, T, Hq, Hkv, D,
+                                           scale, dt, _A, ws, nbytes, None, None)
+    assert chunk(B=0) == 0
+    assert chunk(q=None) == -1 and chunk(table=None) == -1
+    for bad in (dict(Hq=3), dict(T=0), dict(B=70000), dict(ps=20), dict(blocks=0), dict(scale=0.0),
+                dict(scale=-1.0), dict(scale=float("nan")), dict(pages=1 << 30, Hkv=4),
+                dict(T=1 << 30, Hq=8)):
+        assert chunk(**bad) == -2
+    assert chunk(D=96) == -3 and chunk(dt=5) == -3
+    assert chunk(q=_U) == -6 and chunk(ws=_U) == -6
+    assert chunk(nbytes=16) == -4 and chunk(ws=None) == -4
+    size = L.tsd_chunk_attention_workspace_size
+    assert size(2, 4, 4, 2, 64, 16, 2, 1) > 0
+    assert size(0, 4, 4, 2, 64, 16, 2, 1) == 0 and size(2, 4, 3, 2, 64, 16, 2, 1) == 0
+    assert size(4, 4096, 64, 8, 128, 64, 100, 1) == 0      # enough blocks without splitting keys
 
 
 def test_rope_frequencies():

@@ -25,6 +25,8 @@ from .binding import (  # noqa: F401
     VerifyResult,
     attention_plan,
     attention_workspace_size,
+    chunk_attention_paged,
+    chunk_attention_workspace_size,
     device_status,
     exported_symbols,
     kv_commit,

@@ -68,6 +68,9 @@ _SIGNATURES: Dict[str, Tuple[object, list]] = {
     "tsd_rope_append_paged": (_I, [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I, _I,
                                    ctypes.c_float, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P,
                                    _P, _I, _I, _I, _P, _P]),
+    "tsd_chunk_attention_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I, _I]),
+    "tsd_chunk_attention_paged": (_I, [_P, _P, _P, _P, _I, _I, _I, _P, _P, _I, _I, _I, _I, _I,
+                                       ctypes.c_float, _I, _P, _P, _SZ, _P, _P]),
     "tsd_sample": (_I, [_P, _I64, _I, _I, _I, _P, _P, _P, _P, _P, _I, _P, _P, _I64, _P, _P]),
     "tsd_debug_wait_probe": (_I, [_I, ctypes.c_ulonglong, _P, _P, _P]),
 }
@@ -212,6 +215,18 @@ def _workspace_for(device: torch.device, kind: str, nbytes: int,
         return _get_workspace(device, kind, nbytes)
     _need(workspace, "workspace", torch.uint8, (workspace.numel(),), device)
     return workspace
+
+
+def _scratch_for(device: torch.device, kind: str, nbytes: int,
+                 workspace: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
+    """_workspace_for, but nothing for no bytes, and a buffer of its own for a
+    call that is being captured: it then belongs to the graph, so that two
+    graphs never share one and may be replayed side by side."""
+    if workspace is None and nbytes == 0:
+        return None
+    if workspace is None and device.type == "cuda" and torch.cuda.is_current_stream_capturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return _workspace_for(device, kind, nbytes, workspace)
 
 
 def _status_for(device: torch.device, status: Optional[torch.Tensor]) -> torch.Tensor:
@@ -516,6 +531,58 @@ def _pools(k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tens
     _need(v_pages, "v_pages", dtype, (num_pages, Hkv, page_size, D), device)
     _need(block_table, "block_table", torch.int32, (B, max_blocks), device)
     return num_pages, Hkv, page_size, max_blocks
+
+
+def chunk_attention_workspace_size(B: int, Tmax: int, Hq: int, Hkv: int, D: int, page_size: int,
+                                   max_blocks: int, dtype: torch.dtype) -> int:
+    code = TSD_BF16 if dtype == torch.bfloat16 else TSD_F32
+    return int(load_library().tsd_chunk_attention_workspace_size(B, Tmax, Hq, Hkv, D, page_size,
+                                                                 max_blocks, code))
+
+
+def chunk_attention_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                          block_table: torch.Tensor, prefix_len: torch.Tensor,
+                          chunk_len: torch.Tensor, scale: Optional[float] = None,
+                          out: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None,
+                          status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Causal attention of new tokens q [B][Tmax][Hq][D] (chunk_len[b] of them,
+    one for a decode step) over a paged KV cache that holds prefix_len[b]
+    tokens and, behind them, the new tokens' own K/V rows
+    (rope_append_paged); out[B][Tmax][Hq][D], rows beyond chunk_len not
+    written."""
+    lib = load_library()
+    dev = q.device
+    _cuda(dev)
+    if q.dim() != 4:
+        raise ValueError("q must be [B][Tmax][Hq][D]")
+    B, Tmax, Hq, D = q.shape
+    dt = {torch.float32: TSD_F32, torch.bfloat16: TSD_BF16}.get(q.dtype)
+    if dt is None:
+        raise TypeError("q must be float32 or bfloat16")
+    num_pages, Hkv, page_size, max_blocks = _pools(k_pages, v_pages, block_table, q.dtype, B, D,
+                                                   dev)
+    _need(q, "q", q.dtype, (B, Tmax, Hq, D), dev)
+    _need(prefix_len, "prefix_len", torch.int32, (B,), dev)
+    _need(chunk_len, "chunk_len", torch.int32, (B,), dev)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _need(out, "out", q.dtype, (B, Tmax, Hq, D), dev)
+        _apart(out, "out", q, k_pages, v_pages)
+    st = _status_for(dev, status)
+    sc = D ** -0.5 if scale is None else float(scale)
+    with _on(dev):
+        need = int(lib.tsd_chunk_attention_workspace_size(B, Tmax, Hq, Hkv, D, page_size,
+                                                          max_blocks, dt))
+        ws = _scratch_for(dev, "chunk", need, workspace)
+        rc = lib.tsd_chunk_attention_paged(_ptr(q), _ptr(k_pages), _ptr(v_pages),
+                                           _ptr(block_table), num_pages, page_size, max_blocks,
+                                           _ptr(prefix_len), _ptr(chunk_len), B, Tmax, Hq, Hkv, D,
+                                           sc, dt, _ptr(out), _ptr(ws),
+                                           0 if ws is None else ws.numel(), _ptr(st), _stream(dev))
+    _check(rc, "tsd_chunk_attention_paged")
+    return out
 
 
 def kv_commit_paged(k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor,

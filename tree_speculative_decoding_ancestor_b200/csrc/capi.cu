@@ -86,6 +86,19 @@ int cache_row_bytes(int D, int dtype)
     return D >= 1 && D <= 256 && D * es % 16 == 0 && D * es <= 512 ? D * es : 0;
 }
 
+int check_chunk(const tsd::ChunkArgs &a, int num_pages, int page_size, int max_blocks)
+{
+    if (a.B < 0 || a.B > kMaxGridY || a.Tmax < 1 || a.Hq < 1 || a.Hkv < 1 ||
+        a.Hq > (1 << 16) || a.Hq % a.Hkv != 0 ||
+        (long long)a.Tmax * (a.Hq / a.Hkv) > (1LL << 30) || (long long)a.B * a.Hkv > (1 << 24) ||
+        !page_sizes_ok(num_pages, page_size, max_blocks) ||
+        (long long)num_pages * a.Hkv > 0x7fffffffLL)
+        return TSD_ERR_SHAPE;
+    if ((a.dtype != TSD_F32 && a.dtype != TSD_BF16) || (a.D != 64 && a.D != 128))
+        return TSD_ERR_DTYPE;
+    return TSD_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -216,6 +229,49 @@ int tsd_tree_attention_paged(const void *q, const void *k_pages, const void *v_p
     if (workspace_bytes < tsd::simt_attention_workspace(a, sms))
         return TSD_ERR_WORKSPACE;
     return tsd::launch_simt_attention(a, workspace, workspace_bytes, sms, s);
+}
+
+size_t tsd_chunk_attention_workspace_size(int B, int Tmax, int Hq, int Hkv, int D, int page_size,
+                                          int max_blocks, int dtype)
+{
+    tsd::ChunkArgs a{};
+    a.B = B; a.Tmax = Tmax; a.Hq = Hq; a.Hkv = Hkv; a.D = D; a.dtype = dtype;
+    if (B < 1 || check_chunk(a, 1, page_size, max_blocks) != TSD_OK)
+        return 0;
+    a.pages = kv_pages(nullptr, 1, page_size, max_blocks);
+    return tsd::chunk_attention_workspace(a, device_sms());
+}
+
+int tsd_chunk_attention_paged(const void *q, const void *k_pages, const void *v_pages,
+                              const int32_t *block_table, int num_pages, int page_size,
+                              int max_blocks, const int32_t *prefix_len, const int32_t *chunk_len,
+                              int B, int Tmax, int Hq, int Hkv, int D, float scale, int dtype,
+                              void *out, void *workspace, size_t workspace_bytes,
+                              int32_t *dev_status, tsd_stream_t stream)
+{
+    TSD_NVTX_RANGE();
+    tsd::ChunkArgs a;
+    a.q = q; a.k = k_pages; a.v = v_pages; a.prefix_len = prefix_len; a.chunk_len = chunk_len;
+    a.B = B; a.Tmax = Tmax; a.Hq = Hq; a.Hkv = Hkv; a.D = D; a.dtype = dtype; a.scale = scale;
+    a.out = out; a.dev_status = dev_status;
+    const int rc = check_chunk(a, num_pages, page_size, max_blocks);
+    if (rc != TSD_OK)
+        return rc;
+    if (!(scale > 0.f) || scale > 1e30f)   // row maxima are taken before scaling
+        return TSD_ERR_SHAPE;
+    if (B == 0)
+        return TSD_OK;
+    if (!q || !k_pages || !v_pages || !block_table || !prefix_len || !chunk_len || !out)
+        return TSD_ERR_NULL;
+    if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out) ||
+        !aligned16(workspace))
+        return TSD_ERR_ALIGN;
+    a.pages = kv_pages(block_table, num_pages, page_size, max_blocks);
+    const int sms = device_sms();
+    const size_t need = tsd::chunk_attention_workspace(a, sms);
+    if (need > 0 && (!workspace || workspace_bytes < need))
+        return TSD_ERR_WORKSPACE;
+    return tsd::launch_chunk_attention(a, workspace, sms, reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t tsd_tree_verify_workspace_size(int B, int Tmax, int V)

@@ -171,6 +171,19 @@ size_t umma_attention_workspace(const AttnArgs &a, int num_sms);
 int launch_umma_attention(const AttnArgs &a, void *ws, size_t ws_bytes, int num_sms,
                           cudaStream_t stream);
 
+// Causal attention of new tokens over a paged cache.
+struct ChunkArgs {
+    const void *q, *k, *v;
+    const int32_t *prefix_len, *chunk_len;
+    int B, Tmax, Hq, Hkv, D, dtype;
+    float scale;
+    void *out;
+    int32_t *dev_status;
+    KvPages pages;
+};
+size_t chunk_attention_workspace(const ChunkArgs &a, int num_sms);
+int launch_chunk_attention(const ChunkArgs &a, void *ws, int num_sms, cudaStream_t stream);
+
 size_t verify_workspace(int B, int Tmax, int V);
 size_t verify_stochastic_scratch();   // fixed: independent of the shape
 int verify_stochastic_plan(int B, int V, int32_t out[4]);   // teams, K, chunk, CTAs
