@@ -521,7 +521,7 @@ int tsd_rope_append_paged(const void *q, int64_t q_batch, int64_t q_token, const
  * launch.  Weights below 2^-s / 2 are 0 (never drawn).  A row whose logits
  * are all -inf or NaN, whose temperature is not in [0, 1e30] or whose top_p
  * or min_p is NaN sets TSD_DEV_BAD_ROW and gets tokens -1 and probs 0.
- * V is at most 360448.  Host errors: TSD_ERR_NULL, TSD_ERR_SHAPE,
+ * V is at most 393216.  Host errors: TSD_ERR_NULL, TSD_ERR_SHAPE,
  * TSD_ERR_DTYPE, TSD_ERR_CUDA.
  */
 int tsd_sample(const void *logits, int64_t logits_ld, int dtype, int R, int V,

@@ -196,7 +196,7 @@ def test_c_sample_refuses():
     for bad in (dict(logits=None), dict(u=None), dict(tokens=None)):
         assert sample(**bad) == -1
     for bad in (dict(R=-1), dict(V=0), dict(ld=99), dict(pld=99), dict(S=-1), dict(S=1 << 20),
-                dict(V=360449, ld=360449, pld=360449)):
+                dict(V=393217, ld=393217, pld=393217)):
         assert sample(**bad) == -2
     assert sample(dt=2) == -3
 

@@ -115,7 +115,7 @@ def test_off_by_default(cuda_device):
     _check(cuda_device, logits, u)
 
 
-@pytest.mark.parametrize("V", [7, 5000, 50000])
+@pytest.mark.parametrize("V", [7, 257, 600, 768, 800, 1024, 1025, 5000, 50000])
 def test_equal_logits_are_cut_by_token_id(cuda_device, V):
     # V ties: every step of the search holds them all, down to the token ids
     logits = torch.full((6, V), -3.25)
@@ -225,3 +225,29 @@ def test_no_draws_and_no_rows(cuda_device):
     assert torch.allclose(r.probs.cpu(), torch.softmax(logits, 1), atol=1e-6)
     r = tsd.sample(logits[:0].to(cuda_device), u[:0])
     assert r.tokens.shape == (0, 0)
+
+
+@pytest.mark.parametrize("T,k,p", [(1.0, 0, 1.0), (1.0, 5, 1.0), (0.7, 0, 0.5), (1.0, 500, 0.9)])
+def test_every_candidate_at_the_lowest_number(cuda_device, T, k, p):
+    # a mask of the type's lowest value over every entry, -inf beside it
+    V = 2000
+    logits = torch.full((2, V), torch.finfo(torch.float32).min)
+    logits[:, 100:1300] = -math.inf
+    logits[1, 7] = -3.0e38
+    u = torch.rand(2, 5, generator=torch.Generator().manual_seed(3), dtype=torch.float64)
+    _check(cuda_device, logits, u, T=[T] * 2, k=[k] * 2, p=[p] * 2, exact=True)
+
+
+def test_vocabularies_at_the_limits(cuda_device):
+    logits, u = _logits(14, 2, 393216)
+    _check(cuda_device, logits, u, k=[100, 0], p=[1.0, 0.6])
+    with pytest.raises(tsd.TsdError):
+        tsd.sample(torch.zeros(1, 393216 + 1, device=cuda_device), u[:1].to(cuda_device))
+
+
+@pytest.mark.parametrize("k", [1, 32, 33, 64, 128, 129, 255])
+def test_listed_and_searched_rows(cuda_device, k):
+    # top_k around the sizes at which rows are listed whole, with and without top_p
+    logits, u = _logits(k, 6, 30011)
+    _check(cuda_device, logits, u, k=[k] * 6, p=[1.0, 0.9, 0.5, 1.0, 0.99, 0.9], m=[0.0, 0.0, 0.0, 0.2,
+                                                                               0.001, 0.05])

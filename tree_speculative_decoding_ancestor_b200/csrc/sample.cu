@@ -15,29 +15,34 @@
 // (s = 46 at V = 128256) moves it by about 1e-11.
 //
 // A row belongs to a cluster of C CTAs; each loads its chunk of the row once
-// into shared memory, and every later pass reads it there.
+// into shared memory, and every later pass reads it there, a segment to each
+// warp.  Four CTAs of 256 threads share an SM: a search is a chain of short
+// dependent steps, and the others' passes fill its waits.  (1024 rows of 32000
+// with mixed settings: 286 us, 293 us as two CTAs of 512 threads, 450 to 650
+// us where the passes read the row from L2 instead and twice as many rows are
+// in flight.)
 //   1  the largest logit, and a bound below which no entry can be kept: the
-//      threads are grouped into at least top_k groups, and the smallest of the
-//      groups' largest logits has at least top_k entries at or above it
-//      (top_p alone: one thread per group, and the bound holds if the mass
-//      above it turns out to reach top_p)
-//   2  each warp lists the entries at or above the bound in its segment of the
-//      chunk, in token order; with top_k = 50 of 32000 that leaves about 2%,
-//      and the passes below walk these lists
-//   3  a histogram of the listed entries over 1024 equal steps of the logit:
-//      count and mass per step, added up over the cluster; a scan finds the
-//      step in which the k-th entry, or the top_p mass, falls
-//   4  that step's entries (usually a few) are gathered, and every entry sums
-//      the count and mass in front of it; the one at which the limit is
-//      passed is the threshold, as a 64-bit (logit, token id) key.  More than
-//      kList entries: the same histogram over the keys' range inside the
-//      step, ten bits of the key a round, until few are left -- keys are
-//      distinct, so this ends also when all logits are equal
-//   5  the kept sums of each warp's segment, from them each draw's segment,
-//      which its warp walks; the probabilities of the kept entries, over zeros
-//      that were written while the row was being searched
+//      threads' largest logits are sorted; the (top_k / C)-th of each CTA's
+//      256, the least of them over the cluster, has at least top_k entries at
+//      or above it, and not many more (top_p alone: the smallest of all, and
+//      the bound holds if the mass above it turns out to reach top_p)
+//   2  the entries at or above the bound are listed (top_k = 50 of 32000: some
+//      60).  At most kList of them in the row: every CTA sorts them, and one
+//      scan of their weights answers top_k, top_p and min_p; sorted by token
+//      id, another scan answers the draws.  Otherwise:
+//   3  a histogram of the entries above the bound over 256 equal steps of the
+//      logit: count and mass per step, added up over the cluster; a scan finds
+//      the step in which the k-th entry, or the top_p mass, falls
+//   4  that step's entries (usually some tens) are listed and sorted; the one
+//      at which the limit is passed is the threshold, as a 64-bit (logit,
+//      token id) key.  More than kList entries: the same histogram over the
+//      keys' range inside the step, eight bits of the key a round, until few
+//      are left -- keys are distinct, so this ends also when all logits are
+//      equal
+//   5  the probabilities, and the kept sums of each warp's segment; from them
+//      each draw's segment, which its warp walks
 // Bound: the read of the logits and the write of the probabilities; for rows
-// cut by top_p alone, or not at all, the fp64 exponentials of all entries.
+// cut by top_p alone, or not at all, the exponentials of all entries.
 #include <algorithm>
 #include <atomic>
 
@@ -49,27 +54,33 @@ namespace tsd {
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBins = 2 * kThreads;     // steps of a histogram
-constexpr int kList = 512;              // entries gathered at most
+constexpr int kBins = kThreads;         // steps of a histogram, one per thread
+constexpr int kList = kThreads;         // entries listed at most, one per thread
+constexpr int kListTop = kThreads / 2;  // top_k / C up to which listing is tried: about
+                                        // -256 ln(1 - top_k / (256 C)) entries of a CTA pass
 constexpr int kMaxCluster = 8;
-constexpr int kMaxChunk = 45056;        // logits of a CTA, 176 KB of shared memory
-constexpr int kListChunk = 40000;       // up to here there is room for the warps' lists
+constexpr int kMaxChunk = 49152;        // logits of a CTA, 192 KB of shared memory
 constexpr float kReach = 40.f;          // e^-40 2^s < 1/2: weights from there on are 0
 
 typedef unsigned long long u64;
 
 struct Shared {
     double table[kExpTable];
-    u64 mass[kBins];
-    uint32_t count[kBins];
-    u64 key[kList], weight[kList];      // gathered entries of this CTA
-    u64 all_key[kList], all_weight[kList];
-    u64 warp_sum[kWarps];
-    u64 scan_mass[kWarps];
+    union {
+        // Count and mass per step.  A 64-bit add in shared memory is a
+        // compare-and-swap loop, so the mass is kept as three sums of 16, 16
+        // and the remaining bits of the weights: with V 2^s <= 2^63 none
+        // overflows.
+        uint32_t hist[4][kBins];
+        u64 by_rank[kList];             // weights, then cumulative sums
+    };
+    u64 key[kList];                     // listed entries of this CTA
+    u64 swap[2][kThreads];              // of the sorts
+    u64 warp_sum[kWarps], scan_mass[kWarps];
     uint32_t scan_count[kWarps];
-    float warp_hi[kWarps], warp_bound[kWarps];
+    float warp_hi[kWarps];
     float hi, bound;                    // the CTA's largest logit and bound
     u64 rest;                           // the CTA's mass below the bound
     u64 key_hi, key_lo;                 // of the entries in question
@@ -107,123 +118,289 @@ __device__ __forceinline__ u64 order_key(float l, uint32_t token)
     return ((u64)u << 32) | (0xffffffffu - token);
 }
 
+__device__ __forceinline__ float key_logit(u64 key)
+{
+    const uint32_t u = (uint32_t)(key >> 32);
+    return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xffffffffu));
+}
+
+__device__ __forceinline__ uint32_t key_token(u64 key) { return 0xffffffffu - (uint32_t)key; }
+
+// The chunk of the row in shared memory, as this warp sees it.
 struct Row {
-    const float *l;       // this CTA's logits (shared memory)
-    int n, first;         // how many, and the token id of the first
+    const float *l;       // the chunk (-inf behind its end, up to a multiple of four)
+    int first;            // token id of its first logit
+    int s0, s1;           // this warp's segment (s0 a multiple of four)
     int C, rank;
-    float top;            // the row's largest logit
-    double inv_t;
+    bool deep;            // logits so large that top - 45 T is no float next to it
+    float top, low;       // the row's largest logit, and one whose weight is 0
+    double top_d, per_t;  // weight of x: 2^(((x - top) per_t) / 128)
     float step;           // histogram steps per logit unit
-    // what this warp walks: its segment [s0, s1), or `listed` entries of it
-    const uint16_t *list;
-    int s0, s1, listed;   // listed < 0: the whole segment
 
-    __device__ __forceinline__ int entries() const { return listed < 0 ? s1 - s0 : listed; }
-    __device__ __forceinline__ int entry(int i) const { return s0 + (listed < 0 ? i : list[i]); }
-
+    // Logits i .. i + 3 (i a multiple of four); -inf beyond the segment.
+    __device__ __forceinline__ float4 load(int i) const
+    {
+        return i < s1 ? *reinterpret_cast<const float4 *>(l + i)
+                      : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    }
+    // f(i, x) for every four logits x at i of the segment; every lane takes
+    // part in every call (i may be at or beyond s1).
+    template <typename F> __device__ __forceinline__ void walk(F f) const
+    {
+        const int lane = threadIdx.x & 31;
+        for (int i0 = s0; i0 < s1; i0 += 128)
+            f(i0 + 4 * lane, load(i0 + 4 * lane));
+    }
+    // round(2^s exp((x - top) / T)): a = (x - top) 128 / (T ln 2) = n + r with n
+    // an integer, then 2^(n / 128) from the table (scaled by 2^s) and
+    // 2^(r / 128) from its series to degree 4 (|r| <= 1/2: 1.3e-15).  Rounded
+    // to an integer by adding 2^52 (weights are at most 2^50); the conversion
+    // instruction would be slower.
     __device__ __forceinline__ u64 weight(float x, const double *table) const
     {
-        const double d = x == top ? 0.0 : ((double)x - (double)top) * inv_t;   // inf - inf
-        return __double2ull_rn(table_exp(d, table));
+        constexpr double kRound = 6755399441055744.0;   // 1.5 * 2^52
+        constexpr double c1 = 0.6931471805599453 / 128.0, c2 = c1 * c1 / 2.0;
+        constexpr double c3 = c1 * c2 / 3.0, c4 = c1 * c3 / 4.0;
+        double a = ((double)(deep ? x : fmaxf(x, low)) - top_d) * per_t;
+        if (deep)
+            a = fmax(a, -45.0 * 184.6649652337873);
+        const double sum = a + kRound;
+        const double r = a - (sum - kRound);
+        const int n = __double2loint(sum);
+        const double p = r * fma(r, fma(r, fma(r, c4, c3), c2), c1);
+        const double t = table[n & (kExpTable - 1)];
+        const double y = __hiloint2double(__double2hiint(fma(t, p, t)) + ((n >> 7) << 20),
+                                          __double2loint(fma(t, p, t)));
+        return (u64)__double_as_longlong(y + 4503599627370496.0) & 0xfffffffffffffull;
     }
     // Where x falls on the scale of histogram steps; kBins and above: out of
     // reach, weight 0.
-    __device__ __forceinline__ float place(float x) const
-    {
-        return x == top ? 0.f : (top - x) * step;
-    }
+    __device__ __forceinline__ float place(float x) const { return (top - x) * step; }
 };
 
-// The histogram of every CTA added up: thread t has steps 2t and 2t + 1 with
-// what lies in front of each.
-struct Scan {
-    u64 mass[2], before_mass[2];
-    uint32_t count[2], before[2];
-};
-
-__device__ __forceinline__ void combine_and_scan(Shared &sh, int C, Scan &sc,
-                                                 bool with_rest = false, u64 *rest = nullptr)
+__device__ __forceinline__ void mass_in(Shared &sh, int step, u64 w)
 {
-    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    cluster_sync_all();   // the histograms are complete
-    if (with_rest) {
-        u64 all = 0;
-        for (int r = 0; r < C; ++r)
-            all += remote_u64(&sh.rest, r);
-        *rest = all;
-    }
+    atomicAdd(&sh.hist[1][step], (uint32_t)w & 0xffffu);
+    atomicAdd(&sh.hist[2][step], (uint32_t)(w >> 16) & 0xffffu);
+    atomicAdd(&sh.hist[3][step], (uint32_t)(w >> 32));
+}
+
+__device__ __forceinline__ void count_in(Shared &sh, int step) { atomicAdd(&sh.hist[0][step], 1u); }
+
+__device__ __forceinline__ void clear_hist(Shared &sh)
+{
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        sc.mass[i] = 0;
-        sc.count[i] = 0;
-        for (int r = 0; r < C; ++r) {
-            sc.mass[i] += remote_u64(&sh.mass[2 * t + i], r);
-            sc.count[i] += remote_u32(&sh.count[2 * t + i], r);
-        }
-    }
-    u64 m = sc.mass[0] + sc.mass[1];
-    uint32_t c = sc.count[0] + sc.count[1];
-    const u64 own_m = m;
-    const uint32_t own_c = c;
+    for (int i = 0; i < 4; ++i)
+        sh.hist[i][threadIdx.x] = 0u;
+}
+
+// The histogram of every CTA added up: thread t has step t with what lies in
+// front of it.
+struct Scan {
+    u64 mass, before_mass;
+    uint32_t count, before;
+};
+
+// Inclusive sums of v over the threads in front of and including this one;
+// `total` of all.  Ends with a barrier behind the last read.
+__device__ __forceinline__ u64 block_scan(Shared &sh, u64 v, u64 &total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const u64 pm = __shfl_up_sync(0xffffffffu, m, o);
-        const uint32_t pc = __shfl_up_sync(0xffffffffu, c, o);
-        if (lane >= o) {
-            m += pm;
-            c += pc;
-        }
+        const u64 p = __shfl_up_sync(0xffffffffu, v, o);
+        v += lane >= o ? p : 0;
     }
-    if (lane == 31) {
-        sh.scan_mass[warp] = m;
-        sh.scan_count[warp] = c;
+    if (lane == 31)
+        sh.scan_mass[warp] = v;
+    __syncthreads();
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        const u64 m = sh.scan_mass[w];
+        v += w < warp ? m : 0;
+        total += m;
     }
     __syncthreads();
-    m -= own_m;
-    c -= own_c;
-    for (int w = 0; w < warp; ++w) {
-        m += sh.scan_mass[w];
-        c += sh.scan_count[w];
+    return v;
+}
+
+__device__ __forceinline__ void combine_and_scan(Shared &sh, int C, Scan &sc)
+{
+    const int t = threadIdx.x;
+    cluster_sync_all();   // the histograms are complete
+    sc.mass = 0;
+    sc.count = 0;
+#pragma unroll 1
+    for (int r = 0; r < C; r += 2) {
+        uint32_t h[2][4];   // eight remote loads in flight
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                h[i][k] = r + i < C ? remote_u32(&sh.hist[k][t], r + i) : 0u;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            sc.mass += (u64)h[i][1] + ((u64)h[i][2] << 16) + ((u64)h[i][3] << 32);
+            sc.count += h[i][0];
+        }
     }
-    sc.before_mass[0] = m;
-    sc.before[0] = c;
-    sc.before_mass[1] = m + sc.mass[0];
-    sc.before[1] = c + sc.count[0];
     cluster_sync_all();   // every CTA has read the histograms: they may be reused
+    u64 total;
+    sc.before_mass = block_scan(sh, sc.mass, total) - sc.mass;
+    sc.before = (uint32_t)block_scan(sh, sc.count, total) - sc.count;
 }
 
 // Where the limit (an entry count, or a mass) falls; sh.found_* for all.
 // Some step holds it: 0 < limit <= the total.
 __device__ __forceinline__ void find_step(Shared &sh, const Scan &sc, bool by_mass, u64 limit)
 {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const bool here = by_mass ? sc.before_mass[i] < limit &&
-                                        limit <= sc.before_mass[i] + sc.mass[i]
-                                  : sc.before[i] < limit && limit <= sc.before[i] + sc.count[i];
-        if (here) {
-            sh.found_bin = 2 * threadIdx.x + i;
-            sh.found_before = sc.before[i];
-            sh.found_before_mass = sc.before_mass[i];
-            sh.found_count = sc.count[i];
-            sh.found_mass = sc.mass[i];
-        }
+    const bool here = by_mass ? sc.before_mass < limit && limit <= sc.before_mass + sc.mass
+                              : sc.before < limit && limit <= sc.before + sc.count;
+    if (here) {
+        sh.found_bin = threadIdx.x;
+        sh.found_before = sc.before;
+        sh.found_before_mass = sc.before_mass;
+        sh.found_count = sc.count;
+        sh.found_mass = sc.mass;
     }
     __syncthreads();
+}
+
+// Bitonic sort, descending, of one key per thread; n of them count, the others
+// are 0.  Strides within a warp are shuffles; warps of zeros only keep step.
+__device__ __forceinline__ u64 sort_descending(Shared &sh, u64 v, int n)
+{
+    const int t = threadIdx.x;
+    const int n2 = n > 1 ? 1 << (32 - __clz(n - 1)) : 1;   // what the network spans
+    const bool active = (t & ~31) < n2;
+    int buf = 0;
+    __syncthreads();   // the buffers' last readers are done
+#pragma unroll
+    for (int size = 2; size <= kThreads; size <<= 1) {
+        if (size > n2)
+            break;
+#pragma unroll
+        for (int stride = size >> 1; stride > 0; stride >>= 1) {
+            if (stride >= 32) {   // two buffers: one barrier an exchange
+                sh.swap[buf][t] = v;
+                __syncthreads();
+                const u64 w = sh.swap[buf][t ^ stride];
+                buf ^= 1;
+                v = (((t & stride) == 0) == ((t & size) == 0)) == (v > w) ? v : w;
+            } else if (active) {
+                const u64 w = __shfl_xor_sync(0xffffffffu, v, stride);
+                v = (((t & stride) == 0) == ((t & size) == 0)) == (v > w) ? v : w;
+            }
+        }
+    }
+    return v;
+}
+
+// The q-th largest of the threads' values (a bitonic sort of them, unless it is
+// the smallest).  Begins behind the last readers of sh.swap.
+__device__ __forceinline__ float nth_largest(Shared &sh, float v, int q)
+{
+    const int t = threadIdx.x;
+    float *swap = reinterpret_cast<float *>(sh.swap);
+    if (q == kThreads) {
+        v = -warp_max(-v);
+        if ((t & 31) == 0)
+            swap[t >> 5] = v;
+        __syncthreads();
+        return -warp_max((t & 31) < kWarps ? -swap[t & 31] : -INFINITY);
+    }
+    int buf = 0;
+#pragma unroll
+    for (int size = 2; size <= kThreads; size <<= 1)
+#pragma unroll
+        for (int stride = size >> 1; stride > 0; stride >>= 1) {
+            float w;
+            if (stride >= 32) {   // two buffers: one barrier an exchange
+                swap[buf + t] = v;
+                __syncthreads();
+                w = swap[buf + (t ^ stride)];
+                buf ^= kThreads;
+            } else {
+                w = __shfl_xor_sync(0xffffffffu, v, stride);
+            }
+            v = ((t & stride) == 0) == ((t & size) == 0) ? fmaxf(v, w) : fminf(v, w);
+        }
+    if (t == q - 1)
+        swap[2 * kThreads] = v;
+    __syncthreads();
+    return swap[2 * kThreads];
+}
+
+// Every CTA's listed keys, one per thread (0 beyond their number, n).  The
+// lists are complete behind the cluster barrier that this begins with.  More
+// than kList: n alone.
+__device__ __forceinline__ u64 all_keys(Shared &sh, int C, int &n)
+{
+    const int lane = threadIdx.x & 31;
+    cluster_sync_all();
+    uint32_t end = lane < C ? remote_u32(&sh.listed, lane) : 0;   // where a CTA's keys end
+#pragma unroll
+    for (int o = 1; o < kMaxCluster; o <<= 1) {
+        const uint32_t p = __shfl_up_sync(0xffffffffu, end, o);
+        end += lane >= o ? p : 0;
+    }
+    n = (int)min(__shfl_sync(0xffffffffu, end, kMaxCluster - 1), (uint32_t)kList + 1u);
+    int r = 0;
+    uint32_t from = 0;
+#pragma unroll
+    for (int q = 0; q < kMaxCluster - 1; ++q) {
+        const uint32_t x = __shfl_sync(0xffffffffu, end, q);
+        r = threadIdx.x >= x ? q + 1 : r;
+        from = threadIdx.x >= x ? x : from;
+    }
+    return n <= kList && (int)threadIdx.x < n ? remote_u64(&sh.key[threadIdx.x - from], r) : 0;
+}
+
+// The entries of four that are chosen, appended to the CTA's list (counted
+// beyond its end, too).  Every lane of the warp takes part.
+__device__ __forceinline__ void list_in(Shared &sh, const float4 &x, int i, bool c0, bool c1, bool c2,
+                                        bool c3)
+{
+    if (!__any_sync(0xffffffffu, c0 | c1 | c2 | c3))
+        return;
+    const int lane = threadIdx.x & 31;
+    const uint32_t below = (1u << lane) - 1u;
+    const uint32_t b0 = __ballot_sync(0xffffffffu, c0), b1 = __ballot_sync(0xffffffffu, c1);
+    const uint32_t b2 = __ballot_sync(0xffffffffu, c2), b3 = __ballot_sync(0xffffffffu, c3);
+    uint32_t p = 0;
+    if (lane == 0)
+        p = atomicAdd(&sh.listed, (uint32_t)(__popc(b0) + __popc(b1) + __popc(b2) + __popc(b3)));
+    p = __shfl_sync(0xffffffffu, p, 0) + __popc(b0 & below) + __popc(b1 & below) +
+        __popc(b2 & below) + __popc(b3 & below);
+    if (c0 && p < kList)
+        sh.key[p] = order_key(x.x, i);
+    p += c0;
+    if (c1 && p < kList)
+        sh.key[p] = order_key(x.y, i + 1);
+    p += c1;
+    if (c2 && p < kList)
+        sh.key[p] = order_key(x.z, i + 2);
+    p += c2;
+    if (c3 && p < kList)
+        sh.key[p] = order_key(x.w, i + 3);
 }
 
 // The entry of step `bin` (found_count entries behind found_before and
 // found_before_mass) at which the limit is passed.  Returns its key, and in
 // mass_incl the mass up to and including it.
-__device__ u64 resolve(Shared &sh, const Row &row, int bin, bool by_mass, u64 limit, u64 *mass_incl)
+__device__ __forceinline__ u64 resolve(Shared &sh, const Row &row, int bin, bool by_mass, u64 limit,
+                                    u64 *mass_incl)
 {
-    const int lane = threadIdx.x & 31, n_mine = row.entries();
     const float from = (float)bin, to = (float)(bin + 1);
-    auto in_step = [&](float x) {
-        const float f = row.place(x);
-        return f >= from && f < to;
-    };
     u64 lo = 0, hi = ~0ull;   // keys in question
+    auto in_question = [&](float x, int i) {
+        const float f = row.place(x);
+        if (!(f >= from && f < to))
+            return false;
+        const u64 k = order_key(x, row.first + i);
+        return k >= lo && k <= hi;
+    };
     uint32_t count = sh.found_count, before = sh.found_before;
     u64 before_mass = sh.found_before_mass;
     __syncthreads();
@@ -234,23 +411,18 @@ __device__ u64 resolve(Shared &sh, const Row &row, int bin, bool by_mass, u64 li
         }
         __syncthreads();
         u64 khi = 0, klo = ~0ull;
-        for (int e = lane; e < n_mine; e += 32) {
-            const int i = row.entry(e);
-            const float x = row.l[i];
-            if (!in_step(x))
-                continue;
-            const u64 k = order_key(x, row.first + i);
-            if (k < lo || k > hi)
-                continue;
-            khi = max(khi, k);
-            klo = min(klo, k);
-        }
+        row.walk([&](int i, const float4 &x) {
+            const float e[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (in_question(e[j], i + j)) {
+                    khi = max(khi, order_key(e[j], row.first + i + j));
+                    klo = min(klo, order_key(e[j], row.first + i + j));
+                }
+        });
         atomicMax(&sh.key_hi, khi);
         atomicMin(&sh.key_lo, klo);
-        for (int i = threadIdx.x; i < kBins; i += kThreads) {
-            sh.mass[i] = 0;
-            sh.count[i] = 0;
-        }
+        clear_hist(sh);
         cluster_sync_all();
         for (int r = 0; r < row.C; ++r) {
             khi = max(khi, remote_u64(&sh.key_hi, r));
@@ -258,19 +430,17 @@ __device__ u64 resolve(Shared &sh, const Row &row, int bin, bool by_mass, u64 li
         }
         hi = khi;
         lo = klo;
-        const int shift = max(0, 64 - __clzll((long long)(hi - lo)) - 10);   // 1024 steps
-        for (int e = lane; e < n_mine; e += 32) {
-            const int i = row.entry(e);
-            const float x = row.l[i];
-            if (!in_step(x))
-                continue;
-            const u64 k = order_key(x, row.first + i);
-            if (k < lo || k > hi)
-                continue;
-            const int s = (int)((hi - k) >> shift);
-            atomicAdd(&sh.count[s], 1u);
-            atomicAdd(&sh.mass[s], row.weight(x, sh.table));
-        }
+        const int shift = max(0, 64 - __clzll((long long)(hi - lo)) - 8);   // 256 steps
+        row.walk([&](int i, const float4 &x) {
+            const float e[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (in_question(e[j], i + j)) {
+                    const int s = (int)((hi - order_key(e[j], row.first + i + j)) >> shift);
+                    count_in(sh, s);
+                    mass_in(sh, s, row.weight(e[j], sh.table));
+                }
+        });
         Scan sc;
         combine_and_scan(sh, row.C, sc);
         find_step(sh, sc, by_mass, by_mass ? limit - before_mass : limit - before);
@@ -284,99 +454,119 @@ __device__ u64 resolve(Shared &sh, const Row &row, int bin, bool by_mass, u64 li
     if (threadIdx.x == 0)
         sh.listed = 0;
     __syncthreads();
-    for (int e = lane; e < n_mine; e += 32) {
-        const int i = row.entry(e);
-        const float x = row.l[i];
-        if (!in_step(x))
-            continue;
-        const u64 k = order_key(x, row.first + i);
-        if (k < lo || k > hi)
-            continue;
-        const uint32_t at = atomicAdd(&sh.listed, 1u);
-        sh.key[at] = k;
-        sh.weight[at] = row.weight(x, sh.table);
+    row.walk([&](int i, const float4 &x) {
+        list_in(sh, x, row.first + i, in_question(x.x, i), in_question(x.y, i + 1), in_question(x.z, i + 2),
+                in_question(x.w, i + 3));
+    });
+    int n;
+    u64 key = all_keys(sh, row.C, n);
+    key = sort_descending(sh, key, n);
+    const u64 w = key ? row.weight(key_logit(key), sh.table) : 0;
+    u64 all;
+    const u64 incl = before_mass + block_scan(sh, w, all);
+    if (key && (by_mass ? incl - w < limit && limit <= incl : before + threadIdx.x + 1 == limit)) {
+        sh.found_key = key;
+        sh.found_mass = incl;
     }
-    cluster_sync_all();
-    int n = 0;
-    for (int r = 0; r < row.C; ++r) {
-        const int m = (int)remote_u32(&sh.listed, r);
-        for (int i = threadIdx.x; i < m; i += kThreads) {
-            sh.all_key[n + i] = remote_u64(&sh.key[i], r);
-            sh.all_weight[n + i] = remote_u64(&sh.weight[i], r);
-        }
-        n += m;
-    }
-    cluster_sync_all();   // lists read everywhere (and all_* complete here)
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-        const u64 k = sh.all_key[i], w = sh.all_weight[i];
-        u64 m = before_mass;
-        uint32_t c = before;
-        for (int j = 0; j < n; ++j) {
-            const bool ahead = sh.all_key[j] > k;
-            c += ahead ? 1u : 0u;
-            m += ahead ? sh.all_weight[j] : 0ull;
-        }
-        if (by_mass ? m < limit && limit <= m + w : c + 1 == limit) {
-            sh.found_key = k;
-            sh.found_mass = m + w;
-        }
-    }
-    __syncthreads();
+    cluster_sync_all();   // lists read everywhere; found_* complete here
     *mass_incl = sh.found_mass;
-    return sh.found_key;
+    const u64 key_found = sh.found_key;
+    __syncthreads();
+    return key_found;
 }
 
-// Each lane's 4 consecutive entries from i on that are at or above the bound,
-// appended to the warp's list in token order.  Returns the list's new length.
-__device__ __forceinline__ int append(const float4 &x, int i, int left, float bound, uint16_t *list,
-                                      int at, int room)
+// The mass that top_p of `total` asks for: an entry is kept if less lies in
+// front of it.
+__device__ __forceinline__ u64 mass_limit(float top_p, u64 total)
 {
-    const uint32_t below = (1u << (threadIdx.x & 31)) - 1u;
-    const bool c0 = left > 0 && x.x >= bound, c1 = left > 1 && x.y >= bound;
-    const bool c2 = left > 2 && x.z >= bound, c3 = left > 3 && x.w >= bound;
-    if (!__any_sync(0xffffffffu, c0 | c1 | c2 | c3))
-        return at;
-    const uint32_t b0 = __ballot_sync(0xffffffffu, c0), b1 = __ballot_sync(0xffffffffu, c1);
-    const uint32_t b2 = __ballot_sync(0xffffffffu, c2), b3 = __ballot_sync(0xffffffffu, c3);
-    int p = at + __popc(b0 & below) + __popc(b1 & below) + __popc(b2 & below) + __popc(b3 & below);
-    if (c0 && p < room)
-        list[p] = (uint16_t)i;
-    p += c0;
-    if (c1 && p < room)
-        list[p] = (uint16_t)(i + 1);
-    p += c1;
-    if (c2 && p < room)
-        list[p] = (uint16_t)(i + 2);
-    p += c2;
-    if (c3 && p < room)
-        list[p] = (uint16_t)(i + 3);
-    return at + __popc(b0) + __popc(b1) + __popc(b2) + __popc(b3);
+    const u64 want = (u64)fmax(ceil((double)top_p * (double)total), 1.0);
+    return min(max(want, (u64)1), total);
+}
+
+// A weight (below 2^52) as a double, without the slow conversion instruction.
+__device__ __forceinline__ double weight_double(u64 w)
+{
+    return __longlong_as_double((long long)(w | 0x4330000000000000ull)) - 4503599627370496.0;
+}
+
+// A draw takes the first entry whose cumulative sum exceeds this.
+__device__ __forceinline__ u64 draw_at(double u, u64 total)
+{
+    const double x = u * (double)total;
+    return x > 0.0 ? min((u64)x, total - 1) : 0;
+}
+
+// Step 2 behind the listing: n keys of the row, one per thread; the kept ones'
+// probabilities (over zeros) and the draws.  [first, last) are this CTA's
+// tokens, probs its part of the row.
+__device__ __forceinline__ void finish_list(Shared &sh, const SampleArgs &a, const Row &row, u64 key,
+                                            int n, int top_k, float top_p, u64 floor_w, long long r,
+                                            int first, int last, float *probs)
+{
+    const int t = threadIdx.x, k = min(top_k, n);
+    key = sort_descending(sh, key, n);
+    const u64 w = key ? row.weight(key_logit(key), sh.table) : 0;
+    u64 all;
+    const u64 incl = block_scan(sh, w, all);
+    if (t == k - 1)
+        sh.found_mass = incl;
+    __syncthreads();
+    const u64 limit = top_p < 1.f ? mass_limit(top_p, sh.found_mass) : ~0ull;
+    // the kept entries are a prefix of the order
+    const bool keep = t < k && incl - w < limit && w >= floor_w && w > 0;
+    const int kept = __syncthreads_count(keep);
+    if (t == kept - 1)
+        sh.found_before_mass = incl;
+    sh.by_rank[t] = w;
+    __syncthreads();
+    const u64 total = sh.found_before_mass;
+    const int token = (int)key_token(key);
+    if (probs && keep && token >= first && token < last)
+        probs[token - first] = (float)((double)w * (1.0 / (double)total));
+    if (row.rank != 0 || a.S == 0)
+        return;
+    // in token order: the complement of (token, rank), descending
+    const u64 id = sort_descending(
+        sh, keep ? ~(((u64)key_token(key) << 32) | (uint32_t)t) : 0, kept);
+    const u64 cum = block_scan(sh, id ? sh.by_rank[(uint32_t)~id] : 0, all);
+    sh.by_rank[t] = cum;
+    sh.swap[0][t] = ~id >> 32;
+    __syncthreads();
+    for (int s = t; s < a.S; s += kThreads) {
+        const u64 at = draw_at(a.u[r * a.S + s], total);
+        int lo = 0, up = kept - 1;   // first cumulative sum above it
+        while (lo < up) {
+            const int mid = (lo + up) >> 1;
+            if (sh.by_rank[mid] > at)
+                up = mid;
+            else
+                lo = mid + 1;
+        }
+        a.tokens[r * a.S + s] = (int32_t)sh.swap[0][lo];
+    }
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2)
-    sample_kernel(SampleArgs a, int C, int chunk, double scale)
+__global__ void __launch_bounds__(kThreads, 4)
+    sample_kernel(SampleArgs a, int C, int steps, double scale)
 {
-    extern __shared__ uint4 smem_raw[];
-    // the chunk (a multiple of 128 logits), the warps' lists, the rest
-    float *l = reinterpret_cast<float *>(smem_raw);
-    uint16_t *lists = reinterpret_cast<uint16_t *>(l + chunk);
-    const int room = chunk <= kListChunk ? chunk / kWarps / 2 : 0;   // of a warp's list
-    Shared &sh = *reinterpret_cast<Shared *>(lists + room * kWarps);
+    extern __shared__ float4 smem_raw[];
+    Shared &sh = *reinterpret_cast<Shared *>(smem_raw);
+    float *const l = reinterpret_cast<float *>(smem_raw + (sizeof(Shared) + 15) / 16);
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const long long r = blockIdx.x / C;
     Row row;
     row.C = C;
     row.rank = (int)cluster_ctarank();
-    const long long r = blockIdx.x / C;
     row.l = l;
-    row.first = row.rank * chunk;
-    row.n = max(0, min(chunk, a.V - row.first));
-    const int seg = chunk / kWarps;
-    row.s0 = min(warp * seg, row.n);
-    row.s1 = min(row.s0 + seg, row.n);
-    row.listed = -1;
-    uint16_t *const list = lists + warp * room;
-    row.list = list;
+    // whole steps of 128 logits, spread evenly over the cluster's warps
+    auto begin = [&](int w) {
+        return (int)min((long long)steps * w / (C * kWarps) * 128, (long long)a.V);
+    };
+    const int first = begin(row.rank * kWarps), last = begin((row.rank + 1) * kWarps);
+    row.first = first;
+    row.s0 = begin(row.rank * kWarps + warp) - first;
+    row.s1 = begin(row.rank * kWarps + warp + 1) - first;
 
     float T_ = a.temperature ? a.temperature[r] : 1.f;
     int top_k = a.top_k ? a.top_k[r] : 0;
@@ -391,9 +581,28 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     top_k = top_k >= a.V ? 0 : max(top_k, 0);
     const bool cut = top_k > 0 || top_p < 1.f;
+    float *const probs = a.probs ? a.probs + r * a.probs_ld + first : nullptr;
+    const bool probs_vec = (reinterpret_cast<uintptr_t>(probs) & 15u) == 0;
+    auto put4 = [&](int i, float p0, float p1, float p2, float p3) {
+        if (probs_vec && i + 3 < row.s1) {
+            *reinterpret_cast<float4 *>(probs + i) = make_float4(p0, p1, p2, p3);
+            return;
+        }
+        const float p[4] = {p0, p1, p2, p3};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (i + j < row.s1)
+                probs[i + j] = p[j];
+    };
+    auto zeros = [&]() {
+        for (int i = row.s0 + 4 * lane; i < row.s1; i += 128)
+            put4(i, 0.f, 0.f, 0.f, 0.f);
+    };
 
-    // 1: the chunk into shared memory; NaN counts as -inf, -0 as +0
-    const T *src = static_cast<const T *>(a.logits) + r * a.ld + row.first;
+    // 1: the chunk into shared memory, its largest logit and the bound; NaN
+    // counts as -inf, -0 as +0
+    const T *src = static_cast<const T *>(a.logits) + r * a.ld + first;
+    const int n_own = last - first;
     float hi = -INFINITY;
     auto clean = [&](float x) {
         x = fmaxf(x, -INFINITY) + 0.f;
@@ -403,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     constexpr int N = 16 / sizeof(T);
     int done = 0;
     if ((reinterpret_cast<uintptr_t>(src) & 15u) == 0) {   // whole 16-byte vectors
-        const int nv = row.n / N;
+        const int nv = n_own / N;
 #pragma unroll 4
         for (int i = t; i < nv; i += kThreads) {
             union {
@@ -419,53 +628,32 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         done = nv * N;
     }
-    for (int i = done + t; i < row.n; i += kThreads)
-        l[i] = clean(to_float(src[i]));
-    float *const probs = a.probs ? a.probs + r * a.probs_ld + row.first : nullptr;
-    const bool sparse = cut || min_p > 0.f || bad;
-    if (probs && sparse) {   // most stay 0: written while the row is searched
-        int from = row.s0;
-        if ((reinterpret_cast<uintptr_t>(probs) & 15u) == 0) {
-            for (int i = row.s0 + 4 * lane; i + 3 < row.s1; i += 128)
-                *reinterpret_cast<float4 *>(probs + i) = make_float4(0.f, 0.f, 0.f, 0.f);
-            from += (row.s1 - row.s0) & ~3;
-        }
-        for (int i = from + lane; i < row.s1; i += 32)
-            probs[i] = 0.f;
-    }
+    for (int i = done + t; i < ((n_own + 3) & ~3); i += kThreads)
+        l[i] = i < n_own ? clean(to_float(src[i])) : -INFINITY;
     fill_exp_table(sh.table, scale);
-    for (int i = t; i < kBins; i += kThreads) {
-        sh.mass[i] = 0;
-        sh.count[i] = 0;
-    }
-    // groups of g threads, at least top_k of them in the cluster
-    int g = top_k > 0 ? 32 : 1;
-    while (g > 1 && C * kThreads / g < top_k)
-        g >>= 1;
-    float bound = hi;
-    for (int o = 1; o < g; o <<= 1)
-        bound = fmaxf(bound, __shfl_xor_sync(0xffffffffu, bound, o));
-    bound = cut && top_k <= C * kThreads ? -warp_max(-bound) : -INFINITY;
+    clear_hist(sh);
+    if (t == 0)
+        sh.listed = 0;
+    // the bound: the q-th largest of the threads' largest logits, q such that
+    // C of these cover top_k; all threads' without top_k
+    const int q = top_k > 0 ? (top_k + C - 1) / C : kThreads;
+    float bound = -INFINITY;
+    if (cut && q <= kThreads)
+        bound = nth_largest(sh, hi, q);
     hi = warp_max(hi);
-    if (lane == 0) {
+    if (lane == 0)
         sh.warp_hi[warp] = hi;
-        sh.warp_bound[warp] = bound;
-    }
     __syncthreads();
+    hi = warp_max(lane < kWarps ? sh.warp_hi[lane] : -INFINITY);
     if (t == 0) {
-        for (int w = 1; w < kWarps; ++w) {
-            hi = fmaxf(hi, sh.warp_hi[w]);
-            bound = fminf(bound, sh.warp_bound[w]);
-        }
         sh.hi = hi;
         sh.bound = bound;
     }
     cluster_sync_all();
-    for (int q = 0; q < C; ++q) {
-        hi = fmaxf(hi, __uint_as_float(remote_u32(&sh.hi, q)));
-        bound = fminf(bound, __uint_as_float(remote_u32(&sh.bound, q)));
-    }
-    row.top = hi;
+    hi = lane < C ? __uint_as_float(remote_u32(&sh.hi, lane)) : -INFINITY;
+    bound = lane < C ? __uint_as_float(remote_u32(&sh.bound, lane)) : INFINITY;
+    hi = warp_max(hi);
+    bound = -warp_max(-bound);
     bad = bad || !(hi > -INFINITY);
     if (bad) {   // the same on every CTA of the cluster
         if (row.rank == 0) {
@@ -474,48 +662,68 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int s = t; s < a.S; s += kThreads)
                 a.tokens[r * a.S + s] = -1;
         }
-        for (int i = row.s0 + lane; probs && !sparse && i < row.s1; i += 32)
-            probs[i] = 0.f;
+        if (probs)
+            zeros();
         cluster_sync_all();   // no CTA leaves while a peer reads its extremes
         return;
     }
-    row.inv_t = 1.0 / (double)T_;
+    if (hi == INFINITY) {   // +inf stands for 0, everything else for -inf
+        for (int i = t; i < ((n_own + 3) & ~3); i += kThreads)
+            l[i] = l[i] == INFINITY ? 0.f : -INFINITY;
+        hi = 0.f;
+        bound = -INFINITY;
+        __syncthreads();
+    }
+    row.top = hi;
+    row.top_d = (double)hi;
+    row.per_t = 184.6649652337873 / (double)T_;   // 128 / ln 2 / T
+    row.low = hi - 45.f * T_;
+    row.deep = !(fabs((double)hi - (double)row.low - 45.0 * (double)T_) <= (double)T_);
+    row.step = (float)(kBins - 1) / fmaxf(fminf(hi - bound, kReach * T_), 1e-30f);
+    const u64 floor_w = (u64)ceil((double)fminf(fmaxf(min_p, 0.f), 1.f) * scale);
 
-    // 2 .. 4: the threshold
-    u64 threshold = 0;      // kept: keys from here up
-    float keep_from = -INFINITY;   // and so logits from here up
+    // 2: few entries
+    bool some = bound > -INFINITY;
+    if (some && top_k > 0 && q <= kListTop) {
+        row.walk([&](int i, const float4 &x) {
+            list_in(sh, x, first + i, x.x >= bound, x.y >= bound, x.z >= bound, x.w >= bound);
+        });
+        if (probs)
+            zeros();
+        int n;
+        const u64 key = all_keys(sh, C, n);
+        if (n <= kList) {
+            finish_list(sh, a, row, key, n, top_k, top_p, floor_w, r, first, last, probs);
+            cluster_sync_all();   // no CTA leaves while a peer reads its list
+            return;
+        }
+    }
+
+    // 3, 4: the threshold
+    const bool with_mass = top_p < 1.f, with_rest = with_mass && top_k == 0;
+    u64 threshold = 0, total = 0;   // kept: keys from here up
     while (cut) {
-        const bool with_mass = top_p < 1.f, with_rest = with_mass && top_k == 0;
-        const bool all = !(bound > -INFINITY);
-        row.step = (float)(kBins - 1) / fmaxf(fminf(hi - bound, kReach * T_), 1e-30f);
         u64 rest = 0;
-        row.listed = -1;
-        if (!all) {
-            int at = 0;
-            for (int i0 = row.s0; i0 < row.s1; i0 += 128) {
-                const int i = i0 + 4 * lane, left = row.s1 - i;
-                const float4 x = left > 0 ? *reinterpret_cast<const float4 *>(l + i)
-                                          : make_float4(0.f, 0.f, 0.f, 0.f);
-                at = append(x, i - row.s0, left, bound, list, at, room);
-                if (with_rest) {
-                    rest += left > 0 && x.x < bound ? row.weight(x.x, sh.table) : 0;
-                    rest += left > 1 && x.y < bound ? row.weight(x.y, sh.table) : 0;
-                    rest += left > 2 && x.z < bound ? row.weight(x.z, sh.table) : 0;
-                    rest += left > 3 && x.w < bound ? row.weight(x.w, sh.table) : 0;
+        row.walk([&](int i, const float4 &x) {
+            const float e[4] = {x.x, x.y, x.z, x.w};
+            u64 w[4] = {0, 0, 0, 0};
+            if (with_rest) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    w[j] = row.weight(e[j], sh.table);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float f = row.place(e[j]);
+                if (e[j] >= bound && f < (float)kBins) {
+                    count_in(sh, (int)f);
+                    if (with_mass)
+                        mass_in(sh, (int)f, with_rest ? w[j] : row.weight(e[j], sh.table));
+                } else {
+                    rest += w[j];
                 }
             }
-            row.listed = at <= room ? at : -1;
-            __syncwarp();
-        }
-        for (int e = lane; e < row.entries(); e += 32) {
-            const float x = l[row.entry(e)];
-            const float f = row.place(x);
-            if (x < bound || !(f < (float)kBins))
-                continue;
-            atomicAdd(&sh.count[(int)f], 1u);
-            if (with_mass)
-                atomicAdd(&sh.mass[(int)f], row.weight(x, sh.table));
-        }
+        });
         if (with_rest) {
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1)
@@ -525,69 +733,100 @@ __global__ void __launch_bounds__(kThreads, 2)
             __syncthreads();
             if (t == 0) {
                 rest = 0;
+#pragma unroll
                 for (int w = 0; w < kWarps; ++w)
                     rest += sh.warp_sum[w];
                 sh.rest = rest;
             }
         }
         Scan sc;
-        combine_and_scan(sh, C, sc, with_rest, &rest);
+        combine_and_scan(sh, C, sc);
         if (t == kThreads - 1) {
-            sh.found_count = sc.before[1] + sc.count[1];
-            sh.found_mass = sc.before_mass[1] + sc.mass[1];
+            sh.found_count = sc.before + sc.count;
+            sh.found_mass = sc.before_mass + sc.mass;
+        }
+        if (with_rest) {
+            rest = lane < C ? remote_u64(&sh.rest, lane) : 0;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                rest += __shfl_xor_sync(0xffffffffu, rest, o);
         }
         __syncthreads();
         const u64 above = sh.found_mass;
-        u64 total = above + (with_rest ? rest : 0);
         const uint32_t entries = sh.found_count;
+        total = above + (with_rest ? rest : 0);
         __syncthreads();
         if (top_k > 0 && (uint32_t)top_k < entries) {
             find_step(sh, sc, false, (u64)top_k);
             threshold = resolve(sh, row, (int)sh.found_bin, false, (u64)top_k, &total);
-            __syncthreads();
         }
         if (with_mass) {
-            const u64 want = (u64)fmax(ceil((double)top_p * (double)total), 1.0);
-            const u64 limit = min(max(want, (u64)1), total);
+            const u64 limit = mass_limit(top_p, total);
             if (top_k == 0 && limit > above) {   // the mass above the bound is short of top_p
                 bound = -INFINITY;
-                for (int i = t; i < kBins; i += kThreads) {
-                    sh.mass[i] = 0;
-                    sh.count[i] = 0;
-                }
-                __syncthreads();
+                row.step = (float)(kBins - 1) / fmaxf(kReach * T_, 1e-30f);
+                clear_hist(sh);
+                cluster_sync_all();   // and every CTA has read the others' rest
                 continue;
             }
             find_step(sh, sc, true, limit);
-            u64 incl;
-            threshold = resolve(sh, row, (int)sh.found_bin, true, limit, &incl);
-            __syncthreads();
+            threshold = resolve(sh, row, (int)sh.found_bin, true, limit, &total);
         }
         break;
     }
-    if (!cut)
-        row.step = (float)(kBins - 1) / fmaxf(kReach * T_, 1e-30f);
-    if (threshold) {   // the logit of the threshold's key
-        const uint32_t u = (uint32_t)(threshold >> 32);
-        keep_from = __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xffffffffu));
-    }
 
-    // 5: kept sums of the warps' segments
-    const u64 floor_w = (u64)ceil((double)fminf(fmaxf(min_p, 0.f), 1.f) * scale);
-    if (min_p > 0.f)   // no logit below this one (a step's width of margin) has weight min_p
+    // 5: probabilities, kept sums of the warps' segments, draws
+    float keep_from = threshold ? key_logit(threshold) : -INFINITY;
+    // the kept sum is known if top_p was asked for and min_p takes nothing off it
+    const bool known = with_mass && threshold &&
+                       row.weight(keep_from, sh.table) >= floor_w;
+    if (min_p > 0.f)   // no logit below this one (with some margin) has weight min_p
         keep_from = fmaxf(keep_from, __double2float_rd((double)hi + (double)T_ *
                                                        (log((double)fminf(min_p, 1.f)) - 1e-3)));
-    auto kept = [&](int i) -> u64 {   // the weight of entry i, 0 if it is not kept
-        const float x = l[i];
-        if (x < keep_from || !(x > -INFINITY) || order_key(x, row.first + i) < threshold)
-            return 0;
-        const u64 w = row.weight(x, sh.table);
-        return w >= floor_w ? w : 0;
+    auto kept4 = [&](int i, const float4 &x, u64 (&w)[4]) {
+        const float e[4] = {x.x, x.y, x.z, x.w};
+        bool keep[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            keep[j] = e[j] > keep_from || (e[j] == keep_from && e[j] > -INFINITY &&
+                                           order_key(e[j], row.first + i + j) >= threshold);
+            w[j] = 0;
+        }
+        if (!__any_sync(0xffffffffu, keep[0] | keep[1] | keep[2] | keep[3]))
+            return false;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const u64 v = row.weight(e[j], sh.table);
+            w[j] = keep[j] && v >= floor_w ? v : 0;
+        }
+        return true;
     };
-    const int n_mine = row.entries();
     u64 sum = 0;
-    for (int e = lane; e < n_mine; e += 32)
-        sum += kept(row.entry(e));
+    auto write = [&](u64 all, bool count) {
+        const double inv = 1.0 / (double)all;
+        row.walk([&](int i, const float4 &x) {
+            u64 w[4];
+            if (kept4(i, x, w)) {
+                if (count)
+                    sum += (w[0] + w[1]) + (w[2] + w[3]);
+                if (i < row.s1)
+                    put4(i, (float)(weight_double(w[0]) * inv), (float)(weight_double(w[1]) * inv),
+                         (float)(weight_double(w[2]) * inv), (float)(weight_double(w[3]) * inv));
+            } else if (i < row.s1) {
+                put4(i, 0.f, 0.f, 0.f, 0.f);
+            }
+        });
+    };
+    const bool at_once = probs && known;
+    if (at_once) {
+        write(total, true);
+    } else {
+        row.walk([&](int i, const float4 &x) {
+            u64 w[4];
+            if (kept4(i, x, w))
+                sum += (w[0] + w[1]) + (w[2] + w[3]);
+        });
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -595,7 +834,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (lane == 0)
         sh.warp_sum[warp] = sum;
     cluster_sync_all();
-    u64 total = 0, before = 0;   // of the row, and in front of this warp's segment
+    total = 0;
+    u64 before = 0;   // in front of this warp's segment
     for (int i = lane; i < C * kWarps; i += 32) {
         const u64 w = remote_u64(&sh.warp_sum[i % kWarps], i / kWarps);
         total += w;
@@ -606,14 +846,20 @@ __global__ void __launch_bounds__(kThreads, 2)
         total += __shfl_xor_sync(0xffffffffu, total, o);
         before += __shfl_xor_sync(0xffffffffu, before, o);
     }
+    if (probs && !at_once)
+        write(total, false);
     for (int s = 0; s < a.S; ++s) {
-        const double x = a.u[r * a.S + s] * (double)total;
-        const u64 at = x > 0.0 ? min((u64)x, total - 1) : 0;   // first cumulative sum above it
+        const u64 at = draw_at(a.u[r * a.S + s], total);   // first cumulative sum above it
         if (at < before || at >= before + sum)
             continue;
         u64 run = before;
-        for (int e = 0; e < n_mine; e += 32) {
-            u64 c = e + lane < n_mine ? kept(row.entry(e + lane)) : 0;
+        for (int i0 = row.s0; i0 < row.s1; i0 += 128) {
+            const int i = i0 + 4 * lane;
+            u64 w[4];
+            if (!kept4(i, row.load(i), w))
+                continue;
+            const u64 own = (w[0] + w[1]) + (w[2] + w[3]);
+            u64 c = own;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const u64 p = __shfl_up_sync(0xffffffffu, c, o);
@@ -621,30 +867,19 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
             const uint32_t over = __ballot_sync(0xffffffffu, run + c > at);
             if (over) {
-                if (lane == 0)
-                    a.tokens[r * a.S + s] = row.first + row.entry(e + __ffs(over) - 1);
+                if (lane == __ffs(over) - 1) {
+                    u64 m = run + c - own;
+                    int j = 0;
+                    while (j < 3 && m + w[j] <= at)
+                        m += w[j++];
+                    a.tokens[r * a.S + s] = first + i + j;
+                }
                 break;
             }
             run += __shfl_sync(0xffffffffu, c, 31);
         }
     }
-    if (probs) {
-        const double inv = 1.0 / (double)total;
-        __syncwarp();   // the zeros of this warp's segment are written
-        for (int e = lane; e < n_mine; e += 32) {
-            const int i = row.entry(e);
-            const u64 w = kept(i);
-            if (w || !sparse)
-                probs[i] = (float)((double)w * inv);
-        }
-    }
     cluster_sync_all();   // no CTA leaves while a peer reads its sums
-}
-
-// the chunk, half as many 16-bit list entries, the rest
-size_t sample_smem(int chunk)
-{
-    return (size_t)chunk * (chunk <= kListChunk ? 5 : 4) + sizeof(Shared);
 }
 
 }  // namespace
@@ -653,19 +888,20 @@ int sample_max_vocab() { return kMaxCluster * kMaxChunk; }
 
 int launch_sample(const SampleArgs &a, int R, int dtype, int num_sms, cudaStream_t stream)
 {
-    // CTAs per row: as few as hold the row at two CTAs per SM; more (down to
-    // 4096 logits each) while the rows alone leave SMs idle.
+    // CTAs per row: as few as hold the row at four CTAs per SM (8192 logits
+    // each, or what eight of them have to hold); more (down to 2048 logits
+    // each) while the rows alone leave SMs idle.
     int C = 1;
-    while (C < kMaxCluster && (a.V + C - 1) / C > 16384)
+    while (C < kMaxCluster && ((a.V + C - 1) / C > 8192 ||
+                               ((long long)R * C < 2LL * num_sms && a.V / C >= 4096)))
         C *= 2;
-    while (C < kMaxCluster && (long long)R * C < num_sms && (a.V + C - 1) / C > 4096)
-        C *= 2;
-    const int chunk = ((a.V + C - 1) / C + 127) & ~127;   // warps' segments of whole vectors
+    const int steps = (a.V + 127) / 128;
+    const int chunk = (steps + C - 1) / C * 128;   // of a CTA at most
     int log2v = 0;
     while ((1LL << log2v) < a.V)
         ++log2v;
     const int s = std::min(50, 63 - log2v);
-    const size_t smem = sample_smem(chunk);
+    const auto smem = [](int n) { return (sizeof(Shared) + 15) / 16 * 16 + (size_t)n * sizeof(float); };
     auto kern = dtype == TSD_BF16 ? sample_kernel<__nv_bfloat16> : sample_kernel<float>;
     constexpr int kMaxDevices = 64;
     static std::atomic<bool> raised[kMaxDevices][2];
@@ -675,13 +911,13 @@ int launch_sample(const SampleArgs &a, int R, int dtype, int num_sms, cudaStream
         return TSD_ERR_CUDA;
     if (!raised[dev][dtype == TSD_BF16].load()) {
         TSD_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                          (int)std::max(sample_smem(kMaxChunk), sample_smem(kListChunk))));
+                                          (int)smem(kMaxChunk + 256)));
         raised[dev][dtype == TSD_BF16].store(true);
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((long long)R * C));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = smem(chunk);
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -690,8 +926,7 @@ int launch_sample(const SampleArgs &a, int R, int dtype, int num_sms, cudaStream
     at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    const cudaError_t err = cudaLaunchKernelEx(&cfg, kern, a, C, chunk, ldexp(1.0, s));
-    if (err != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, kern, a, C, steps, ldexp(1.0, s)) != cudaSuccess) {
         (void)cudaGetLastError();
         return TSD_ERR_CUDA;
     }
