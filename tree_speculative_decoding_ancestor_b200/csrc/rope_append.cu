@@ -8,14 +8,19 @@
 // with pairs (i, i + rot/2) or (2i, 2i + 1); dimensions from rot on pass
 // through.  The angle is a product of a position that may need 20 bits and a
 // frequency: its fp32 rounding alone would be 2^-24 * 10^5 = 0.006 radians,
-// so it is formed and reduced to [-pi, pi] in fp64; the cosine and sine are
+// so it is formed and reduced to half a turn in fp64; the cosine and sine are
 // fp32, and each output is rounded once.
 //
 // Every row is read and written once: HBM-bound for chunks, launch latency
-// for single tokens.  A thread keeps one 16-byte slot of a row (and that
-// slot's cosines and sines in registers) and walks the heads of its token
-// with it, so the trigonometry and its shared-memory reads are paid once per
-// token and not per head.
+// for single tokens.  A thread keeps two 16-byte slots of a row -- for pairs
+// (i, i + rot/2) the two that hold each other's partners -- with their cosines
+// and sines in registers, and walks the heads of its token with them, so the
+// trigonometry and its shared-memory reads are paid once per token and not per
+// head, and no element is loaded twice.  Measured (bf16, D = 128, 64/8 heads):
+// 4096 tokens 33.3 us = 5.0 TB/s, 77% of a plain copy; 2048 tree tokens 15.7
+// us; 8 single tokens 2.8 us.  One slot a thread, its partners loaded again:
+// 37.6 and 19.8 us; two or four rows in flight, three or six CTAs per SM: 34 to
+// 73 us and 15 to 28 (spills where the registers end).
 #include <algorithm>
 
 #include "tsd_common.cuh"
@@ -26,6 +31,8 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeTokens = 4;      // tokens per CTA at most
+constexpr int kRopeRows = 3;        // rows a thread has in flight
+constexpr int kRopeCtas = 4;        // CTAs per SM
 constexpr int kRopeMaxPairs = 128;  // rot / 2 at most (rows of 512 bytes, 16-bit elements)
 
 template <typename T> struct Vec16 {
@@ -37,8 +44,12 @@ template <typename T> struct Vec16 {
     __device__ Vec16() {}
 };
 
-template <typename T, bool INTERLEAVED>
-__global__ void __launch_bounds__(kRopeThreads)
+// How the pairs of a head lie: (2i, 2i + 1), or (i, i + rot / 2) with the
+// partners of a 16-byte slot a slot themselves, or anywhere.
+enum Pairs { kInterleaved, kHalves, kOddHalves };
+
+template <typename T, Pairs P_>
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
     rope_append_kernel(RopeArgs a, int tokens_per_cta, int heads_per_cta)
 {
     constexpr int N = Vec16<T>::N;
@@ -59,13 +70,10 @@ __global__ void __launch_bounds__(kRopeThreads)
     for (int i = threadIdx.x; i < (t1 - t0) * half; i += kRopeThreads) {
         const int t = i / half, p = i - t * half;
         const int off = a.depth ? a.depth[(size_t)b * a.Tmax + t0 + t] - 1 : t0 + t;
-        const double angle = (double)((long long)P + off) * a.inv_freq[p];
-        const double turns = rint(angle * 0.15915494309189535);   // 1 / (2 pi)
-        // 2 pi as the sum of two doubles: the reduced angle keeps fp32 accuracy
-        double r = fma(turns, -6.283185307179586, angle);
-        r = fma(turns, -2.4492935982947064e-16, r);
+        // in turns, of which only the part behind the point matters
+        const double turns = (double)((long long)P + off) * a.inv_freq[p] * 0.15915494309189535;
         float s, c;
-        sincosf((float)r, &s, &c);
+        sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
         s_cos[t][p] = c * a.rot_scale;
         s_sin[t][p] = s * a.rot_scale;
     }
@@ -80,86 +88,119 @@ __global__ void __launch_bounds__(kRopeThreads)
                                 : -1;
     }
     __syncthreads();
-    const int slots = a.D / N;   // 16-byte slots of a row
-    const int par = kRopeThreads / slots;
-    const int j = threadIdx.x % slots, hp = threadIdx.x / slots;
+    const int slots = a.D / N, units = (slots + 1) / 2;   // 16-byte slots of a row, two a thread
+    const int par = kRopeThreads / units;                 // rows side by side
+    const int j = threadIdx.x % units, hp = threadIdx.x / units;
     if (hp >= par)
         return;
-    const int e0 = j * N;
+    // this thread's slots: partners, or the next two
+    const int turned = P_ == kHalves ? half / N : 0;
+    const int sa = P_ == kHalves ? (j < turned ? j : 2 * j) : 2 * j;
+    const int sb = P_ == kHalves && j < turned ? j + turned : sa + 1;
+    const bool two = sb < slots;
+    const int ea = sa * N, eb = sb * N;
     const int h_end = min((int)(blockIdx.z + 1) * heads_per_cta, a.Hq + 2 * a.Hkv);
-    const bool paired = !INTERLEAVED && half % N == 0;   // a slot's partners are a slot
     for (int t = t0; t < t1; ++t) {
-        float c[N], s[N];   // out = x * c + partner * s
+        // cosines and sines: of slot a's N pairs (halves), or of the N / 2 pairs
+        // of each slot (interleaved)
+        float c[N], s[N];
+        if (P_ != kOddHalves) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int e = e0 + i;
-            const bool turn = e < a.rot;
-            const int p = !turn ? 0 : INTERLEAVED ? e >> 1 : (e < half ? e : e - half);
-            const bool first = INTERLEAVED ? (e & 1) == 0 : e < half;
-            c[i] = turn ? s_cos[t - t0][p] : 1.f;
-            s[i] = turn ? (first ? -s_sin[t - t0][p] : s_sin[t - t0][p]) : 0.f;
+            for (int i = 0; i < N; ++i) {
+                const int p = P_ == kHalves ? ea + i : ea / 2 + i;
+                const bool turn = P_ == kHalves ? j < turned : p < half;
+                c[i] = turn ? s_cos[t - t0][p] : 1.f;
+                s[i] = turn ? s_sin[t - t0][p] : 0.f;
+            }
         }
         const long long row = s_row[t - t0];
-#pragma unroll 4
-        for (int h = blockIdx.z * heads_per_cta + hp; h < h_end; h += par) {
-            const bool is_q = h < a.Hq, is_k = !is_q && h < a.Hq + a.Hkv;
-            const int hk = h - a.Hq - (is_k ? 0 : a.Hkv);   // KV head (k and v rows)
-            if (!is_q && row < 0)
-                continue;
-            const T *src =
-                is_q   ? static_cast<const T *>(a.q) + b * a.q_batch + t * a.q_token + (size_t)h * a.D
-                : is_k ? static_cast<const T *>(a.k) + b * a.k_batch + t * a.k_token + (size_t)hk * a.D
-                       : static_cast<const T *>(a.v) + b * a.v_batch + t * a.v_token + (size_t)hk * a.D;
-            Vec16<T> x, y;
-            x.raw = *reinterpret_cast<const uint4 *>(src + e0);
-            const bool turn = (is_q || is_k) && e0 < a.rot;
-            if (turn) {
-                float f[N];
+        const T *const q = static_cast<const T *>(a.q) + b * a.q_batch + t * a.q_token;
+        const T *const k = static_cast<const T *>(a.k) + b * a.k_batch + t * a.k_token;
+        const T *const v = static_cast<const T *>(a.v) + b * a.v_batch + t * a.v_token;
+        const bool turn = P_ == kHalves ? j < turned : ea < a.rot;
+        auto source = [&](int h) {
+            return h < a.Hq            ? q + (size_t)h * a.D
+                   : h < a.Hq + a.Hkv ? k + (size_t)(h - a.Hq) * a.D
+                                      : v + (size_t)(h - a.Hq - a.Hkv) * a.D;
+        };
+        for (int h0 = blockIdx.z * heads_per_cta + hp; h0 < h_end; h0 += kRopeRows * par) {
+            // all rows' loads in flight before the first is used
+            Vec16<T> x[kRopeRows], y[kRopeRows];
 #pragma unroll
-                for (int i = 0; i < N; ++i)
-                    f[i] = to_float(x.e[i]);
-                if (INTERLEAVED) {
+            for (int i = 0; i < kRopeRows; ++i) {
+                const int h = h0 + i * par;
+                if (h >= h_end)
+                    continue;
+                const T *const src = source(h);
+                x[i].raw = __ldg(reinterpret_cast<const uint4 *>(src + ea));
+                if (two)
+                    y[i].raw = __ldg(reinterpret_cast<const uint4 *>(src + eb));
+            }
 #pragma unroll
-                    for (int i = 0; i < N; ++i)
-                        y.e[i] = from_float<T>(f[i] * c[i] + f[i ^ 1] * s[i]);
-                } else if (paired) {
-                    Vec16<T> o;
-                    o.raw = *reinterpret_cast<const uint4 *>(src + (e0 < half ? e0 + half : e0 - half));
+            for (int i = 0; i < kRopeRows; ++i) {
+                const int h = h0 + i * par;
+                if (h >= h_end || (h >= a.Hq && row < 0))
+                    continue;
+                if (turn && h < a.Hq + a.Hkv) {
+                    if (P_ == kHalves) {
 #pragma unroll
-                    for (int i = 0; i < N; ++i)
-                        y.e[i] = from_float<T>(f[i] * c[i] + to_float(o.e[i]) * s[i]);
-                } else {
+                        for (int n = 0; n < N; ++n) {
+                            const float f = to_float(x[i].e[n]), g = to_float(y[i].e[n]);
+                            x[i].e[n] = from_float<T>(f * c[n] - g * s[n]);
+                            y[i].e[n] = from_float<T>(g * c[n] + f * s[n]);
+                        }
+                    } else if (P_ == kInterleaved) {
 #pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        const int e = e0 + i;
-                        const float o =
-                            e < a.rot ? to_float(src[e < half ? e + half : e - half]) : 0.f;
-                        y.e[i] = e < a.rot ? from_float<T>(f[i] * c[i] + o * s[i]) : x.e[i];
+                        for (int n = 0; n < N; n += 2) {   // dimensions from rot on stay as they are
+                            if (ea + n < a.rot) {
+                                const float f = to_float(x[i].e[n]), g = to_float(x[i].e[n + 1]);
+                                x[i].e[n] = from_float<T>(f * c[n / 2] - g * s[n / 2]);
+                                x[i].e[n + 1] = from_float<T>(g * c[n / 2] + f * s[n / 2]);
+                            }
+                            if (eb + n < a.rot) {
+                                const int m = (N + n) / 2;
+                                const float f = to_float(y[i].e[n]), g = to_float(y[i].e[n + 1]);
+                                y[i].e[n] = from_float<T>(f * c[m] - g * s[m]);
+                                y[i].e[n + 1] = from_float<T>(g * c[m] + f * s[m]);
+                            }
+                        }
+                    } else {   // element by element
+                        const T *const src = source(h);
+                        for (int n = 0; n < 2 * N; ++n) {
+                            const int e = ea + n;
+                            if (e >= a.rot)
+                                break;
+                            const int p = e < half ? e : e - half;
+                            const float f = to_float(src[e]);
+                            const float g = to_float(src[e < half ? e + half : p]);
+                            const float z = f * s_cos[t - t0][p] +
+                                            (e < half ? -g : g) * s_sin[t - t0][p];
+                            if (n < N)
+                                x[i].e[n] = from_float<T>(z);
+                            else
+                                y[i].e[n - N] = from_float<T>(z);
+                        }
                     }
                 }
-                // dimensions from rot on inside the slot pass through bit for bit
-                if (e0 + N > a.rot) {
-#pragma unroll
-                    for (int i = 0; i < N; ++i)
-                        if (e0 + i >= a.rot)
-                            y.e[i] = x.e[i];
+                T *dst;
+                long long at, extent;
+                if (h < a.Hq) {
+                    at = (((long long)b * a.Tmax + t) * a.Hq + h) * a.D;
+                    extent = (long long)gridDim.y * a.Tmax * a.Hq * a.D;
+                    dst = static_cast<T *>(a.q_out);
+                } else {
+                    const bool is_k = h < a.Hq + a.Hkv;
+                    at = (row + (long long)(h - a.Hq - (is_k ? 0 : a.Hkv)) * a.pages.page_size) *
+                         a.D;
+                    extent = kv_rows_total(a.pages, gridDim.y, a.Hkv, 0) * a.D;
+                    dst = static_cast<T *>(is_k ? a.k_pages : a.v_pages);
                 }
-            } else {
-                y.raw = x.raw;
+                if (in_bounds(at, extent - a.D + 1, a.dev_status)) {
+                    *reinterpret_cast<uint4 *>(dst + at + ea) = x[i].raw;
+                    if (two)
+                        *reinterpret_cast<uint4 *>(dst + at + eb) = y[i].raw;
+                }
             }
-            T *dst;
-            long long at, extent;
-            if (is_q) {
-                at = (((long long)b * a.Tmax + t) * a.Hq + h) * a.D + e0;
-                extent = (long long)gridDim.y * a.Tmax * a.Hq * a.D;
-                dst = static_cast<T *>(a.q_out);
-            } else {
-                at = (row + (long long)hk * a.pages.page_size) * a.D + e0;
-                extent = kv_rows_total(a.pages, gridDim.y, a.Hkv, 0) * a.D;
-                dst = static_cast<T *>(is_k ? a.k_pages : a.v_pages);
-            }
-            if (in_bounds(at, extent - N + 1, a.dev_status))
-                *reinterpret_cast<uint4 *>(dst + at) = y.raw;
         }
     }
 }
@@ -172,7 +213,8 @@ int launch_rope_append(const RopeArgs &a, int B, int dtype, int num_sms, cudaStr
     // grid would leave SMs without a CTA; then the heads are divided too, down
     // to one pass of the CTA's threads over them.
     const int heads = a.Hq + 2 * a.Hkv;
-    const int par = kRopeThreads / (a.D * (dtype == TSD_F32 ? 4 : 2) / 16);
+    const int slots = a.D * (dtype == TSD_F32 ? 4 : 2) / 16;
+    const int par = kRopeThreads / ((slots + 1) / 2);
     int per = kRopeTokens;
     while (per > 1 && (long long)B * ((a.Tmax + per - 1) / per) < 2LL * num_sms)
         per >>= 1;
@@ -181,11 +223,14 @@ int launch_rope_append(const RopeArgs &a, int B, int dtype, int num_sms, cudaStr
     const int hpc = (heads + parts - 1) / parts;
     parts = (heads + hpc - 1) / hpc;
     const dim3 grid((a.Tmax + per - 1) / per, B, parts);
+    const bool whole = a.rot / 2 % (dtype == TSD_F32 ? 4 : 8) == 0;
     auto kern = dtype == TSD_BF16
-                    ? (a.interleaved ? rope_append_kernel<__nv_bfloat16, true>
-                                     : rope_append_kernel<__nv_bfloat16, false>)
-                    : (a.interleaved ? rope_append_kernel<float, true>
-                                     : rope_append_kernel<float, false>);
+                    ? (a.interleaved ? rope_append_kernel<__nv_bfloat16, kInterleaved>
+                       : whole       ? rope_append_kernel<__nv_bfloat16, kHalves>
+                                     : rope_append_kernel<__nv_bfloat16, kOddHalves>)
+                    : (a.interleaved ? rope_append_kernel<float, kInterleaved>
+                       : whole       ? rope_append_kernel<float, kHalves>
+                                     : rope_append_kernel<float, kOddHalves>);
     kern<<<grid, kRopeThreads, 0, stream>>>(a, per, hpc);
     TSD_LAUNCH_CHECK();
     return TSD_OK;
