@@ -55,11 +55,10 @@ __device__ __forceinline__ int block_tiles(const Sizes &z, int rb, int T, int P)
 {
     if (T < 1 || T > z.Tmax || P < 0 || P > z.Lmax - T)
         return 0;
-    const int G = z.Hq / z.Hkv;
-    const long long R = (long long)T * G, r0 = (long long)rb * BQ;
+    const int G = z.Hq / z.Hkv, R = T * G, r0 = rb * BQ;   // at most 2^30 rows
     if (r0 >= R)
         return 0;
-    const int t_last = (int)((min(r0 + BQ, R) - 1) / G);
+    const int t_last = (min(r0 + BQ, R) - 1) / G;
     return (P + t_last + BN) / BN;   // ceil of P + t_last + 1 keys
 }
 
@@ -121,8 +120,9 @@ __device__ __forceinline__ bool find_piece(const Sizes &z, const int32_t *prefix
             w.rb = w.item - w.b * z.nrb;
             w.T = chunk_len[w.b];
             w.P = prefix_len[w.b];
-            w.tile0 = (int)((long long)all * s / w.pieces);
-            w.tile1 = (int)((long long)all * (s + 1) / w.pieces);
+            const int each = all / w.pieces, more = all - each * w.pieces;
+            w.tile0 = s * each + min(s, more);
+            w.tile1 = w.tile0 + each + (s < more ? 1 : 0);
             w.first = first * z.Hkv + w.hk;   // the CTA of piece 0; the others Hkv apart
             return true;
         }
@@ -242,8 +242,8 @@ __global__ void __launch_bounds__(192, kMinBlocks)
     } else {
         const int quarter = warp & 3, tr = quarter * 32 + lane;   // row of the block
         const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-        const long long r = (long long)w.rb * BQ + tr, R = (long long)w.T * G;
-        const int t = (int)(min(r, R - 1) / G), h = w.hk * G + (int)(min(r, R - 1) % G);
+        const int r = w.rb * BQ + tr, R = w.T * G;
+        const int t = min(r, R - 1) / G, h = w.hk * G + min(r, R - 1) - t * G;
         const size_t row = ((size_t)w.b * z.Tmax + t) * z.Hq + h;
         const bool row_ok =
             r < R && in_bounds((long long)row, (long long)z.B * z.Tmax * z.Hq, dev_status);
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(192, kMinBlocks)
         warp_arrive(su.bars.q_full());
         CausalVis vis;
         vis.end = w.P + t + 1;
-        vis.all = w.P + (int)((long long)w.rb * BQ / G) + 1;
+        vis.all = w.P + w.rb * BQ / G + 1;
         const uint32_t taddr_o = su.tmem + lane_off + kO;
         float m_run = -INFINITY, l_run = 0.f;
         bool ok = true;
@@ -296,17 +296,28 @@ __global__ void __launch_bounds__(192, kMinBlocks)
 
 // ------------------------------------------------------------------- fp32
 // BQ rows by 64 keys a tile, 256 threads.  Scores: thread (i, j) of a 16 x 16
-// grid has BQ/16 rows by 4 keys; output: BQ/16 rows by D/16 dims.  Q and K
-// are kept transposed in shared memory so that a step over the head dimension
-// reads 16-byte vectors.  BQ = 16 for decode and short chunks (a 64-row tile
-// would spend four times the FMAs of the KV stream's time), 64 otherwise.
+// grid has BQ/16 rows by the keys j, j + 16, j + 32, j + 48; output: the same
+// rows by D/16 dims.  All operands are read as 16-byte vectors along the head
+// dimension (rows padded by 16 bytes: no bank conflicts), 12 shared-memory
+// wavefronts for 64 FMAs of a warp at BQ = 64, so the FMA pipes are the bound.
+// The next tile's keys and values are copied (cp.async) while this one is
+// computed.  BQ = 16 for decode and short chunks (a 64-row tile would spend
+// four times the FMAs of the KV stream's time), 64 otherwise.
 constexpr int kFmaThreads = 256;
 constexpr int kFmaKeys = 64;
 
-template <int BQ_, int D> constexpr size_t fma_smem()
+template <int BQ_, int D> struct FmaSmem {
+    static constexpr int LD = D + 4, LP = kFmaKeys + 4;   // row steps, in floats
+    static constexpr int kQ = 0, kK = kQ + BQ_ * LD, kV = kK + 2 * kFmaKeys * LD,
+                         kP = kV + 2 * kFmaKeys * D, kFloats = kP + BQ_ * LP;
+    static constexpr size_t kBytes = sizeof(float) * kFloats;
+};
+
+__device__ __forceinline__ void copy16(float *dst, const float *src, bool ok)
 {
-    return sizeof(float) * ((size_t)D * (BQ_ + 4) + (size_t)D * (kFmaKeys + 4) +
-                            (size_t)kFmaKeys * D + (size_t)BQ_ * (kFmaKeys + 4) + kFmaKeys);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ptx::smem_addr(dst)),
+                 "l"(src), "r"(ok ? 16 : 0)
+                 : "memory");   // zeros where there is no key
 }
 
 template <int BQ_, int D>
@@ -316,13 +327,11 @@ __global__ void __launch_bounds__(kFmaThreads)
                           const int32_t *__restrict__ chunk_len, Sizes z, float scale_log2,
                           float *__restrict__ out, Parts parts, int32_t *dev_status, KvPages pages)
 {
+    using Sm = FmaSmem<BQ_, D>;
     constexpr int BN = kFmaKeys, RT = BQ_ / 16, DT = D / 16;   // rows, dims of a thread
+    constexpr int LD = Sm::LD, LP = Sm::LP, VEC = D / 4;
     extern __shared__ float smem[];
-    float *sQ = smem;                       // [D][BQ + 4]
-    float *sK = sQ + D * (BQ_ + 4);         // [D][BN + 4]
-    float *sV = sK + D * (BN + 4);          // [BN][D]
-    float *sP = sV + BN * D;                // [BQ][BN + 4]
-    int *s_row = reinterpret_cast<int *>(sP + BQ_ * (BN + 4));   // [BN] page of a key, -1: none
+    float *const sQ = smem + Sm::kQ, *const sP = smem + Sm::kP;
     check_headers(z, prefix_len, chunk_len, dev_status);
     Piece w;
     if (!find_piece<BQ_, BN>(z, prefix_len, chunk_len, w))
@@ -331,16 +340,43 @@ __global__ void __launch_bounds__(kFmaThreads)
     const int tid = threadIdx.x, ti = tid >> 4, tj = tid & 15;
     if (z.slots && blockIdx.x == (unsigned)w.first && tid == 0)
         parts.meta[w.item * z.Hkv + w.hk] = make_int2(w.first, w.pieces);
-    const long long r0 = (long long)w.rb * BQ_, R = (long long)w.T * G;
+    const int r0 = w.rb * BQ_, R = w.T * G;
     auto out_row = [&](int lr) {   // row of q and out of local row lr
-        const long long r = min(r0 + lr, R - 1);
-        return ((size_t)w.b * z.Tmax + r / G) * z.Hq + w.hk * G + r % G;
+        const int r = min(r0 + lr, R - 1), t = r / G;
+        return ((size_t)w.b * z.Tmax + t) * z.Hq + w.hk * G + r - t * G;
     };
-    for (int i = tid; i < BQ_ * D; i += kFmaThreads) {
-        const int lr = i / D, d = i % D;
+    auto fetch = [&](int kt) {   // the copies of tile kt
+        float *const sK = smem + Sm::kK + (kt & 1) * BN * LD;
+        float *const sV = smem + Sm::kV + (kt & 1) * BN * D;
+#pragma unroll 4
+        for (int i = tid; i < BN * VEC; i += kFmaThreads) {
+            const int j = i / VEC, c = i % VEC, pos = kt * BN + j;
+            bool ok = pos < seq_end;
+            long long row = 0;
+            if (ok) {
+                const int page =
+                    pages.table[(size_t)w.b * pages.max_blocks + (pos >> pages.log2_page)];
+                ok = page >= 0 && page < pages.num_pages;
+                if (ok)
+                    row = ((long long)page * z.Hkv + w.hk) * pages.page_size +
+                          (pos & (pages.page_size - 1));
+                else if (c == 0)
+                    flag(dev_status, TSD_DEV_BAD_PAGE);   // that key reads as zero
+                ok = ok && in_bounds(row, kv_rows_total(pages, z.B, z.Hkv, 0), dev_status);
+            }
+            copy16(sK + j * LD + 4 * c, kp + row * D + 4 * c, ok);
+            copy16(sV + j * D + 4 * c, vp + row * D + 4 * c, ok);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    fetch(w.tile0);
+    for (int i = tid; i < BQ_ * VEC; i += kFmaThreads) {
+        const int lr = i / VEC, c = i % VEC;
         const bool ok = r0 + lr < R && in_bounds((long long)out_row(lr),
                                                  (long long)z.B * z.Tmax * z.Hq, dev_status);
-        sQ[d * (BQ_ + 4) + lr] = ok ? q[out_row(lr) * D + d] : 0.f;
+        const float4 x = ok ? __ldg(reinterpret_cast<const float4 *>(q + out_row(lr) * D) + c)
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
+        *reinterpret_cast<float4 *>(sQ + lr * LD + 4 * c) = x;
     }
     float o[RT][DT], m[RT], l[RT];
     int end[RT];   // keys the row sees
@@ -348,44 +384,20 @@ __global__ void __launch_bounds__(kFmaThreads)
     for (int a = 0; a < RT; ++a) {
         m[a] = -INFINITY;
         l[a] = 0.f;
-        end[a] = w.P + (int)(min(r0 + ti * RT + a, R - 1) / G) + 1;
+        end[a] = w.P + min(r0 + ti * RT + a, R - 1) / G + 1;
 #pragma unroll
         for (int c = 0; c < DT; ++c)
             o[a][c] = 0.f;
     }
     for (int kt = w.tile0; kt < w.tile1; ++kt) {
         const int pos0 = kt * BN;
-        __syncthreads();   // the previous tile is read
-        if (tid < BN) {
-            const int pos = pos0 + tid;
-            int page = -1;
-            if (pos < seq_end) {
-                page = pages.table[(size_t)w.b * pages.max_blocks + (pos >> pages.log2_page)];
-                if (page < 0 || page >= pages.num_pages) {
-                    flag(dev_status, TSD_DEV_BAD_PAGE);   // that key reads as zero
-                    page = -1;
-                }
-            }
-            s_row[tid] = page;
-        }
-        __syncthreads();
-        for (int i = tid; i < BN * (D / 4); i += kFmaThreads) {
-            const int j = i / (D / 4), c = i % (D / 4);
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-            if (s_row[j] >= 0) {
-                const long long row =
-                    ((long long)s_row[j] * z.Hkv + w.hk) * pages.page_size +
-                    ((pos0 + j) & (pages.page_size - 1));
-                if (in_bounds(row, kv_rows_total(pages, z.B, z.Hkv, 0), dev_status)) {
-                    x = __ldg(reinterpret_cast<const float4 *>(kp + row * D) + c);
-                    y = __ldg(reinterpret_cast<const float4 *>(vp + row * D) + c);
-                }
-            }
-            sK[(4 * c + 0) * (BN + 4) + j] = x.x;
-            sK[(4 * c + 1) * (BN + 4) + j] = x.y;
-            sK[(4 * c + 2) * (BN + 4) + j] = x.z;
-            sK[(4 * c + 3) * (BN + 4) + j] = x.w;
-            *reinterpret_cast<float4 *>(sV + j * D + 4 * c) = y;
+        const float *const sK = smem + Sm::kK + (kt & 1) * BN * LD;
+        const float *const sV = smem + Sm::kV + (kt & 1) * BN * D;
+        if (kt + 1 < w.tile1) {   // into the buffers that the barrier below the tile before freed
+            fetch(kt + 1);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+        } else {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
         }
         __syncthreads();
         float s[RT][4];
@@ -394,27 +406,22 @@ __global__ void __launch_bounds__(kFmaThreads)
 #pragma unroll
             for (int c = 0; c < 4; ++c)
                 s[a][c] = 0.f;
-#pragma unroll 8
-        for (int d = 0; d < D; ++d) {
-            float x[RT];
-            if (RT == 4) {
-                const float4 v = *reinterpret_cast<const float4 *>(sQ + d * (BQ_ + 4) + ti * 4);
-                x[0] = v.x;
-                x[RT > 1 ? 1 : 0] = v.y;
-                x[RT > 2 ? 2 : 0] = v.z;
-                x[RT > 3 ? 3 : 0] = v.w;
-            } else {
+#pragma unroll 4
+        for (int d = 0; d < D; d += 4) {
+            float4 y[4];
 #pragma unroll
-                for (int a = 0; a < RT; ++a)
-                    x[a] = sQ[d * (BQ_ + 4) + ti * RT + a];
-            }
-            const float4 y = *reinterpret_cast<const float4 *>(sK + d * (BN + 4) + tj * 4);
+            for (int c = 0; c < 4; ++c)
+                y[c] = *reinterpret_cast<const float4 *>(sK + (tj + 16 * c) * LD + d);
 #pragma unroll
             for (int a = 0; a < RT; ++a) {
-                s[a][0] = fmaf(x[a], y.x, s[a][0]);
-                s[a][1] = fmaf(x[a], y.y, s[a][1]);
-                s[a][2] = fmaf(x[a], y.z, s[a][2]);
-                s[a][3] = fmaf(x[a], y.w, s[a][3]);
+                const float4 x = *reinterpret_cast<const float4 *>(sQ + (ti * RT + a) * LD + d);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    s[a][c] = fmaf(x.x, y[c].x, s[a][c]);
+                    s[a][c] = fmaf(x.y, y[c].y, s[a][c]);
+                    s[a][c] = fmaf(x.z, y[c].z, s[a][c]);
+                    s[a][c] = fmaf(x.w, y[c].w, s[a][c]);
+                }
             }
         }
         // a row's 64 scores are on 16 lanes of one half warp
@@ -423,7 +430,7 @@ __global__ void __launch_bounds__(kFmaThreads)
             float mx = -INFINITY;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                s[a][c] = pos0 + tj * 4 + c < end[a] ? s[a][c] * scale_log2 : -INFINITY;
+                s[a][c] = pos0 + tj + 16 * c < end[a] ? s[a][c] * scale_log2 : -INFINITY;
                 mx = fmaxf(mx, s[a][c]);
             }
 #pragma unroll
@@ -433,12 +440,12 @@ __global__ void __launch_bounds__(kFmaThreads)
             const float base = m_new == -INFINITY ? 0.f : m_new;   // nothing visible yet
             const float alpha = exp2f(m[a] - base);
             float sum = 0.f;
-            float4 p;
-            p.x = exp2f(s[a][0] - base);
-            p.y = exp2f(s[a][1] - base);
-            p.z = exp2f(s[a][2] - base);
-            p.w = exp2f(s[a][3] - base);
-            sum = (p.x + p.y) + (p.z + p.w);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const float p = exp2f(s[a][c] - base);
+                sum += p;
+                sP[(ti * RT + a) * LP + tj + 16 * c] = p;
+            }
 #pragma unroll
             for (int k = 8; k > 0; k >>= 1)
                 sum += __shfl_xor_sync(0xffffffffu, sum, k);
@@ -447,29 +454,31 @@ __global__ void __launch_bounds__(kFmaThreads)
 #pragma unroll
             for (int c = 0; c < DT; ++c)
                 o[a][c] *= alpha;
-            *reinterpret_cast<float4 *>(sP + (ti * RT + a) * (BN + 4) + tj * 4) = p;
         }
         __syncwarp();   // a row's probabilities stay within its half warp
-#pragma unroll 4
-        for (int j = 0; j < BN; ++j) {
-            float y[DT];
+#pragma unroll 2
+        for (int j = 0; j < BN; j += 4) {
+            float4 p[RT];
 #pragma unroll
-            for (int c = 0; c < DT; c += 4) {
-                const float4 v =
-                    *reinterpret_cast<const float4 *>(sV + j * D + (c / 4) * 64 + tj * 4);
-                y[c] = v.x;
-                y[c + 1] = v.y;
-                y[c + 2] = v.z;
-                y[c + 3] = v.w;
-            }
+            for (int a = 0; a < RT; ++a)
+                p[a] = *reinterpret_cast<const float4 *>(sP + (ti * RT + a) * LP + j);
 #pragma unroll
-            for (int a = 0; a < RT; ++a) {
-                const float p = sP[(ti * RT + a) * (BN + 4) + j];
+            for (int k = 0; k < 4; ++k)
 #pragma unroll
-                for (int c = 0; c < DT; ++c)
-                    o[a][c] = fmaf(p, y[c], o[a][c]);
-            }
+                for (int c = 0; c < DT; c += 4) {
+                    const float4 y = *reinterpret_cast<const float4 *>(sV + (j + k) * D +
+                                                                       (c / 4) * 64 + tj * 4);
+#pragma unroll
+                    for (int a = 0; a < RT; ++a) {
+                        const float f = k == 0 ? p[a].x : k == 1 ? p[a].y : k == 2 ? p[a].z : p[a].w;
+                        o[a][c] = fmaf(f, y.x, o[a][c]);
+                        o[a][c + 1] = fmaf(f, y.y, o[a][c + 1]);
+                        o[a][c + 2] = fmaf(f, y.z, o[a][c + 2]);
+                        o[a][c + 3] = fmaf(f, y.w, o[a][c + 3]);
+                    }
+                }
         }
+        __syncthreads();   // this tile's buffers may be refilled
     }
 #pragma unroll
     for (int a = 0; a < RT; ++a) {
@@ -493,63 +502,81 @@ __global__ void __launch_bounds__(kFmaThreads)
 // One warp per row of a block that was split: weights 2^(m_i - max m) over its
 // pieces (Hkv CTAs apart), the weighted sum of their rows over the weighted sum
 // of their sums.  A piece none of whose keys the row sees has sum 0.
+constexpr int kJoinRows = 8;   // rows (warps) of a CTA
+
 template <typename T, int D, int BQ_>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(32 * kJoinRows)
     chunk_join_kernel(Parts parts, const int32_t *__restrict__ prefix_len,
                       const int32_t *__restrict__ chunk_len, Sizes z, T *__restrict__ out,
                       int32_t *dev_status)
 {
-    constexpr int DL = D / 32;
-    const int item = blockIdx.x / z.Hkv, hk = blockIdx.x % z.Hkv;
-    const int b = item / z.nrb, rb = item % z.nrb;
-    const int n_tok = chunk_len[b], P = prefix_len[b];
-    if (block_tiles<BQ_, 64>(z, rb, n_tok, P) == 0)
+    constexpr int DL = D / 32;   // dims of a lane
+    const int item = blockIdx.x / z.Hkv, hk = blockIdx.x - item * z.Hkv;
+    const int b = item / z.nrb, rb = item - b * z.nrb;
+    const int n_tok = chunk_len[b], G = z.Hq / z.Hkv;
+    const int lr = blockIdx.y * kJoinRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (block_tiles<BQ_, 64>(z, rb, n_tok, prefix_len[b]) == 0 || rb * BQ_ + lr >= n_tok * G ||
+        lr >= z.part_rows)
         return;
     const int2 meta = parts.meta[blockIdx.x];
     if (meta.y < 2)
         return;
-    const int G = z.Hq / z.Hkv, lane = threadIdx.x & 31;
-    const long long r0 = (long long)rb * BQ_;
-    const int rows = (int)min((long long)BQ_, (long long)n_tok * G - r0);
-    for (int lr = threadIdx.x >> 5; lr < rows; lr += 4) {
-        float M = -INFINITY;
-        for (int i = lane; i < meta.y; i += 32) {
-            const float2 ml = parts.ml[(size_t)(meta.x + i * z.Hkv) * z.part_rows + lr];
-            M = fmaxf(M, ml.y > 0.f ? ml.x : -INFINITY);
-        }
-        M = warp_max(M);
-        float acc[DL], L = 0.f;
+    float M = -INFINITY;
+    for (int i = lane; i < meta.y; i += 32) {
+        const float2 ml = parts.ml[(size_t)(meta.x + i * z.Hkv) * z.part_rows + lr];
+        M = fmaxf(M, ml.y > 0.f ? ml.x : -INFINITY);
+    }
+    M = warp_max(M);
+    float acc[DL], L = 0.f;
 #pragma unroll
-        for (int k = 0; k < DL; ++k)
-            acc[k] = 0.f;
-#pragma unroll 4
-        for (int i = 0; i < meta.y; ++i) {
-            const size_t at = (size_t)(meta.x + i * z.Hkv) * z.part_rows + lr;
-            const float2 ml = parts.ml[at];
-            const float f = ml.y > 0.f ? exp2f(ml.x - M) : 0.f;
+    for (int k = 0; k < DL; ++k)
+        acc[k] = 0.f;
+    for (int i0 = 0; i0 < meta.y; i0 += 32) {
+        float f = 0.f;   // lane's piece: its weight
+        if (i0 + lane < meta.y) {
+            const float2 ml = parts.ml[(size_t)(meta.x + (i0 + lane) * z.Hkv) * z.part_rows + lr];
+            f = ml.y > 0.f ? exp2f(ml.x - M) : 0.f;
             L = fmaf(f, ml.y, L);
-#pragma unroll
-            for (int k = 0; k < DL; ++k) {
-                const float x = parts.o[at * D + lane + 32 * k];
-                acc[k] = f > 0.f ? fmaf(f, x, acc[k]) : acc[k];
-            }
         }
-        const long long r = r0 + lr;
-        const size_t row = ((size_t)b * z.Tmax + r / G) * z.Hq + hk * G + r % G;
-        const float inv = L > 0.f ? 1.f / L : 0.f;
-        if (in_bounds((long long)row, (long long)z.B * z.Tmax * z.Hq, dev_status))
+        const int n = min(32, meta.y - i0);
+#pragma unroll 8
+        for (int i = 0; i < n; ++i) {
+            const float w = __shfl_sync(0xffffffffu, f, i);
+            const size_t at = (size_t)(meta.x + (i0 + i) * z.Hkv) * z.part_rows + lr;
+            float x[DL];
+            if (DL == 2) {
+                const float2 v = *reinterpret_cast<const float2 *>(parts.o + at * D + lane * DL);
+                x[0] = v.x;
+                x[1] = v.y;
+            } else {
+                const float4 v = *reinterpret_cast<const float4 *>(parts.o + at * D + lane * DL);
+                x[0] = v.x;
+                x[1] = v.y;
+                x[DL > 2 ? 2 : 0] = v.z;
+                x[DL > 3 ? 3 : 0] = v.w;
+            }
 #pragma unroll
             for (int k = 0; k < DL; ++k)
-                out[row * D + lane + 32 * k] = from_float<T>(acc[k] * inv);
+                acc[k] = w > 0.f ? fmaf(w, x[k], acc[k]) : acc[k];
+        }
     }
+    L = warp_sum(L);
+    const int r = rb * BQ_ + lr;
+    const size_t row = ((size_t)b * z.Tmax + r / G) * z.Hq + hk * G + r % G;
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    if (in_bounds((long long)row, (long long)z.B * z.Tmax * z.Hq, dev_status))
+#pragma unroll
+        for (int k = 0; k < DL; ++k)
+            out[row * D + lane * DL + k] = from_float<T>(acc[k] * inv);
 }
 
 // -------------------------------------------------------------------- host
 struct Plan {
     Sizes z;
     bool paired;        // bf16: 64-key tiles, two CTAs per SM
-    int bq, items;
+    int bq;
     long long grid;
+    dim3 join;          // grid of the join
     size_t meta_bytes, ml_bytes, o_bytes;
 };
 
@@ -572,17 +599,18 @@ Plan chunk_plan(const ChunkArgs &a, int num_sms)
     // the last wave mostly empty (fewer than four blocks a slot).
     const int slots = num_sms * (f32 || p.paired ? 2 : 1);
     const long long blocks = (long long)a.B * a.Hkv * p.z.nrb;
-    p.items = 0;
+    size_t items = 0;
     if (blocks < 4LL * slots) {
         p.z.slots = slots;
-        p.items = a.B * p.z.nrb;
+        items = (size_t)a.B * p.z.nrb;
+        p.join = dim3((unsigned)(items * a.Hkv), (p.z.part_rows + kJoinRows - 1) / kJoinRows);
         p.grid = (long long)slots + blocks + a.Hkv;
     } else {
         p.z.slots = 0;
         p.grid = blocks;
     }
     auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
-    p.meta_bytes = p.z.slots ? up((size_t)p.items * a.Hkv * sizeof(int2)) : 0;
+    p.meta_bytes = p.z.slots ? up(items * a.Hkv * sizeof(int2)) : 0;
     p.ml_bytes = p.z.slots ? up((size_t)p.grid * p.z.part_rows * sizeof(float2)) : 0;
     p.o_bytes = p.z.slots ? (size_t)p.grid * p.z.part_rows * a.D * sizeof(float) : 0;
     return p;
@@ -619,10 +647,10 @@ cudaError_t set_smem_attributes()
         {(const void *)chunk_attn_umma_kernel<Wide<64>, 3, 1>, Wide<64>::kSmemBytes},
         {(const void *)chunk_attn_umma_kernel<Half<128>, 2, 2>, Half<128>::kSmemBytes},
         {(const void *)chunk_attn_umma_kernel<Half<64>, 2, 2>, Half<64>::kSmemBytes},
-        {(const void *)chunk_attn_fma_kernel<16, 64>, fma_smem<16, 64>()},
-        {(const void *)chunk_attn_fma_kernel<64, 64>, fma_smem<64, 64>()},
-        {(const void *)chunk_attn_fma_kernel<16, 128>, fma_smem<16, 128>()},
-        {(const void *)chunk_attn_fma_kernel<64, 128>, fma_smem<64, 128>()}};
+        {(const void *)chunk_attn_fma_kernel<16, 64>, FmaSmem<16, 64>::kBytes},
+        {(const void *)chunk_attn_fma_kernel<64, 64>, FmaSmem<64, 64>::kBytes},
+        {(const void *)chunk_attn_fma_kernel<16, 128>, FmaSmem<16, 128>::kBytes},
+        {(const void *)chunk_attn_fma_kernel<64, 128>, FmaSmem<64, 128>::kBytes}};
     for (const auto &k : all)
         if (err == cudaSuccess)
             err = raise_smem(k.kern, k.bytes, true);
@@ -649,7 +677,7 @@ int launch_umma(const ChunkArgs &a, const Plan &p, const Parts &parts, float sl2
         static_cast<__nv_bfloat16 *>(a.out), parts, a.dev_status, a.pages);
     TSD_LAUNCH_CHECK();
     if (p.z.slots) {
-        chunk_join_kernel<__nv_bfloat16, D, BQ><<<p.items * a.Hkv, 128, 0, stream>>>(
+        chunk_join_kernel<__nv_bfloat16, D, BQ><<<p.join, 32 * kJoinRows, 0, stream>>>(
             parts, a.prefix_len, a.chunk_len, p.z, static_cast<__nv_bfloat16 *>(a.out),
             a.dev_status);
         TSD_LAUNCH_CHECK();
@@ -661,13 +689,14 @@ template <int BQ_, int D>
 int launch_fma(const ChunkArgs &a, const Plan &p, const Parts &parts, float sl2,
                cudaStream_t stream)
 {
-    chunk_attn_fma_kernel<BQ_, D><<<(unsigned)p.grid, kFmaThreads, fma_smem<BQ_, D>(), stream>>>(
+    chunk_attn_fma_kernel<BQ_, D>
+        <<<(unsigned)p.grid, kFmaThreads, FmaSmem<BQ_, D>::kBytes, stream>>>(
         static_cast<const float *>(a.q), static_cast<const float *>(a.k),
         static_cast<const float *>(a.v), a.prefix_len, a.chunk_len, p.z, sl2,
         static_cast<float *>(a.out), parts, a.dev_status, a.pages);
     TSD_LAUNCH_CHECK();
     if (p.z.slots) {
-        chunk_join_kernel<float, D, BQ_><<<p.items * a.Hkv, 128, 0, stream>>>(
+        chunk_join_kernel<float, D, BQ_><<<p.join, 32 * kJoinRows, 0, stream>>>(
             parts, a.prefix_len, a.chunk_len, p.z, static_cast<float *>(a.out), a.dev_status);
         TSD_LAUNCH_CHECK();
     }
