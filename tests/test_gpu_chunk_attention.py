@@ -139,6 +139,21 @@ def test_long_prefixes_are_split(cuda_device, dtype, B, Hq, Hkv, D, T, P):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,Hkv,T,P", [(148, 1, 1, 40), (37, 8, 1, 700), (300, 2, 2, 90), (5, 3, 200, 3),
+                                       (64, 2, 70, 500), (2, 64, 1, 2500)])
+def test_ranges_over_many_blocks(cuda_device, dtype, B, Hkv, T, P):
+    # ranges that hold several blocks, cut some, and skip sequences without tokens
+    prefix = [(P * (7 * b + 3)) % (P + 1) for b in range(B)]
+    new = [0 if b % 5 == 4 else 1 + (3 * b) % T for b in range(B)]
+    _check(_case(B + T, DTYPES[dtype], 2 * Hkv, Hkv, 64, 16, prefix, new, T, cuda_device))
+
+
+def test_no_tokens_at_all(cuda_device):
+    for dt in DTYPES.values():
+        _check(_case(3, dt, 4, 2, 64, 16, [0, 33], [0, 0], 3, cuda_device))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_scores_that_rise_and_dominate(cuda_device, dtype):
     # each later key scores higher (the running maximum moves at every tile),
     # one key dwarfs the rest, and a scale of its own
