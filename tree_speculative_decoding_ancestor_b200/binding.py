@@ -26,6 +26,7 @@ LIB_PATH = os.environ.get("TSD_LIBRARY") or os.path.join(_HERE, "lib", "libtsd.s
 TSD_OK = 0
 TSD_F32, TSD_BF16 = 0, 1
 TSD_MAX_TREE = 128
+_CODES = {torch.float32: TSD_F32, torch.bfloat16: TSD_BF16}   # element types and their codes
 TSD_TREE_INVALID = -2
 DEV_BAD_TREE, DEV_BAD_TOKEN, DEV_BAD_QROW, DEV_BAD_PREFIX, DEV_TIMEOUT = 1, 2, 4, 8, 16
 DEV_BAD_PATH, DEV_BAD_PAGE, DEV_BOUNDS, DEV_BAD_ROW = 32, 64, 128, 256
@@ -233,7 +234,8 @@ def _status_for(device: torch.device, status: Optional[torch.Tensor]) -> torch.T
     """The caller's status word (an int32 tensor on the device), or the
     per-device one."""
     if status is None:
-        return device_status(device)
+        st = _status.get(device.index)
+        return device_status(device) if st is None else st
     if not isinstance(status, torch.Tensor) or status.dtype != torch.int32 or \
             status.device != device or status.numel() < 1:
         raise ValueError(f"status must be an int32 tensor on {device}")
@@ -533,6 +535,10 @@ def _pools(k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tens
     return num_pages, Hkv, page_size, max_blocks
 
 
+# Workspace bytes by (sizes, element type, device): they depend on nothing else.
+_chunk_scratch: Dict[Tuple, int] = {}
+
+
 def chunk_attention_workspace_size(B: int, Tmax: int, Hq: int, Hkv: int, D: int, page_size: int,
                                    max_blocks: int, dtype: torch.dtype) -> int:
     code = TSD_BF16 if dtype == torch.bfloat16 else TSD_F32
@@ -557,7 +563,7 @@ def chunk_attention_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch
     if q.dim() != 4:
         raise ValueError("q must be [B][Tmax][Hq][D]")
     B, Tmax, Hq, D = q.shape
-    dt = {torch.float32: TSD_F32, torch.bfloat16: TSD_BF16}.get(q.dtype)
+    dt = _CODES.get(q.dtype)
     if dt is None:
         raise TypeError("q must be float32 or bfloat16")
     num_pages, Hkv, page_size, max_blocks = _pools(k_pages, v_pages, block_table, q.dtype, B, D,
@@ -573,14 +579,17 @@ def chunk_attention_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch
     st = _status_for(dev, status)
     sc = D ** -0.5 if scale is None else float(scale)
     with _on(dev):
-        need = int(lib.tsd_chunk_attention_workspace_size(B, Tmax, Hq, Hkv, D, page_size,
-                                                          max_blocks, dt))
+        sizes = (B, Tmax, Hq, Hkv, D, page_size, max_blocks, dt, dev.index)
+        need = _chunk_scratch.get(sizes)
+        if need is None:
+            need = int(lib.tsd_chunk_attention_workspace_size(*sizes[:-1]))
+            _chunk_scratch[sizes] = need
         ws = _scratch_for(dev, "chunk", need, workspace)
-        rc = lib.tsd_chunk_attention_paged(_ptr(q), _ptr(k_pages), _ptr(v_pages),
-                                           _ptr(block_table), num_pages, page_size, max_blocks,
-                                           _ptr(prefix_len), _ptr(chunk_len), B, Tmax, Hq, Hkv, D,
-                                           sc, dt, _ptr(out), _ptr(ws),
-                                           0 if ws is None else ws.numel(), _ptr(st), _stream(dev))
+        rc = lib.tsd_chunk_attention_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+                                           block_table.data_ptr(), num_pages, page_size, max_blocks,
+                                           prefix_len.data_ptr(), chunk_len.data_ptr(), B, Tmax, Hq, Hkv, D,
+                                           sc, dt, out.data_ptr(), _ptr(ws),
+                                           0 if ws is None else ws.numel(), st.data_ptr(), _stream(dev))
     _check(rc, "tsd_chunk_attention_paged")
     return out
 
@@ -595,7 +604,7 @@ def kv_commit_paged(k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: t
     lib = load_library()
     dev = k_pages.device
     _cuda(dev)
-    dt = {torch.float32: TSD_F32, torch.bfloat16: TSD_BF16}.get(k_pages.dtype)
+    dt = _CODES.get(k_pages.dtype)
     if dt is None:
         raise TypeError("k_pages must be float32 or bfloat16")
     B, Tmax = result.out_path.shape
@@ -607,14 +616,15 @@ def kv_commit_paged(k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: t
     _need(result.n_accepted, "n_accepted", torch.int32, (B,), dev)
     if new_prefix_len is None:
         new_prefix_len = torch.empty((B,), dtype=torch.int32, device=dev)
-    _need(new_prefix_len, "new_prefix_len", torch.int32, (B,), dev)
-    _apart(new_prefix_len, "new_prefix_len", prefix_len)
+    else:
+        _need(new_prefix_len, "new_prefix_len", torch.int32, (B,), dev)
+        _apart(new_prefix_len, "new_prefix_len", prefix_len)
     st = _status_for(dev, status)
     with _on(dev):
-        rc = lib.tsd_kv_commit_paged(_ptr(k_pages), _ptr(v_pages), _ptr(block_table), num_pages,
-                                     page_size, max_blocks, _ptr(prefix_len),
-                                     _ptr(result.out_path), _ptr(result.n_accepted), B, Tmax, Hkv,
-                                     D, dt, _ptr(new_prefix_len), _ptr(st), _stream(dev))
+        rc = lib.tsd_kv_commit_paged(k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), num_pages,
+                                     page_size, max_blocks, prefix_len.data_ptr(),
+                                     result.out_path.data_ptr(), result.n_accepted.data_ptr(), B, Tmax, Hkv,
+                                     D, dt, new_prefix_len.data_ptr(), st.data_ptr(), _stream(dev))
     _check(rc, "tsd_kv_commit_paged")
     return new_prefix_len
 
@@ -664,27 +674,23 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[str]
                            1.0 if rot_scale is None else float(rot_scale))
 
 
-def _need_rows(t: torch.Tensor, name: str, dtype: torch.dtype, shape: Tuple[int, ...],
-               device: torch.device) -> None:
-    """As _need, but only each token's rows [H][D] must be dense."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if (t.shape[3] > 1 and t.stride(3) != 1) or (t.shape[2] > 1 and t.stride(2) != t.shape[3]):
-        raise ValueError(f"{name}: the rows of a token must be contiguous")
-
-
-def _strides(t: torch.Tensor) -> Tuple[int, int]:
-    """Elements from one sequence and one token to the next ([B][T][H][D]); a
-    dimension of one has no step, and gets the dense one."""
-    row = t.shape[2] * t.shape[3]
-    token = t.stride(1) if t.shape[1] > 1 else row
-    return (t.stride(0) if t.shape[0] > 1 else t.shape[1] * token), token
+def _token_rows(t: torch.Tensor, name: str, dtype: torch.dtype, shape: Tuple[int, int, int, int],
+                device: torch.device) -> Tuple[int, int]:
+    """As _need, but only each token's rows [H][D] must be dense; returns the
+    elements from one sequence, and from one token, to the next ([B][T][H][D];
+    a dimension of one has no step, and gets the dense one)."""
+    B, T, H, D = shape
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device:
+        if t.is_contiguous():
+            return T * H * D, H * D
+        batch, token, head, element = t.stride()
+        if (D > 1 and element != 1) or (H > 1 and head != D):
+            raise ValueError(f"{name}: the rows of a token must be contiguous")
+        if T == 1:
+            token = H * D
+        return (batch if B > 1 else T * token), token
+    _need(t, name, dtype, shape, device)
+    raise ValueError(f"{name} must have shape {shape}")   # not reached: _need refuses
 
 
 def rope_append_paged(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, inv_freq: torch.Tensor,
@@ -705,31 +711,33 @@ def rope_append_paged(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, inv_fre
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q must be [B][Tmax][Hq][D] and k, v [B][Tmax][Hkv][D]")
     B, Tmax, Hq, D = q.shape
-    dt = {torch.float32: TSD_F32, torch.bfloat16: TSD_BF16}.get(q.dtype)
+    dt = _CODES.get(q.dtype)
     if dt is None:
         raise TypeError("q must be float32 or bfloat16")
     num_pages, Hkv, page_size, max_blocks = _pools(k_pages, v_pages, block_table, q.dtype, B, D,
                                                    dev)
-    _need_rows(q, "q", q.dtype, (B, Tmax, Hq, D), dev)
-    _need_rows(k, "k", q.dtype, (B, Tmax, Hkv, D), dev)
-    _need_rows(v, "v", q.dtype, (B, Tmax, Hkv, D), dev)
-    _need(inv_freq, "inv_freq", torch.float64, (inv_freq.numel(),), dev)
+    q_batch, q_token = _token_rows(q, "q", q.dtype, (B, Tmax, Hq, D), dev)
+    k_batch, k_token = _token_rows(k, "k", q.dtype, (B, Tmax, Hkv, D), dev)
+    v_batch, v_token = _token_rows(v, "v", q.dtype, (B, Tmax, Hkv, D), dev)
+    pairs = inv_freq.numel()
+    _need(inv_freq, "inv_freq", torch.float64, (pairs,), dev)
     _need(prefix_len, "prefix_len", torch.int32, (B,), dev)
     _need(n_new, "n_new", torch.int32, (B,), dev)
     if depth is not None:
         _need(depth, "depth", torch.int32, (B, Tmax), dev)
     if out is None:
         out = torch.empty((B, Tmax, Hq, D), dtype=q.dtype, device=dev)
-    _need(out, "out", q.dtype, (B, Tmax, Hq, D), dev)
-    _apart(out, "out", q, k, v, k_pages, v_pages)
+    else:
+        _need(out, "out", q.dtype, (B, Tmax, Hq, D), dev)
+        _apart(out, "out", q, k, v, k_pages, v_pages)
     st = _status_for(dev, status)
     with _on(dev):
         rc = lib.tsd_rope_append_paged(
-            _ptr(q), *_strides(q), _ptr(k), *_strides(k), _ptr(v), *_strides(v), _ptr(inv_freq),
-            2 * inv_freq.numel(), int(bool(interleaved)), float(rot_scale), _ptr(prefix_len),
-            _ptr(n_new), _ptr(depth), B, Tmax, Hq, Hkv, D, dt, _ptr(out), _ptr(k_pages),
-            _ptr(v_pages), _ptr(block_table), num_pages, page_size, max_blocks, _ptr(st),
-            _stream(dev))
+            q.data_ptr(), q_batch, q_token, k.data_ptr(), k_batch, k_token, v.data_ptr(), v_batch,
+            v_token, inv_freq.data_ptr(), 2 * pairs, int(bool(interleaved)), float(rot_scale),
+            prefix_len.data_ptr(), n_new.data_ptr(), _ptr(depth), B, Tmax, Hq, Hkv, D, dt,
+            out.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
+            num_pages, page_size, max_blocks, st.data_ptr(), _stream(dev))
     _check(rc, "tsd_rope_append_paged")
     return out
 
@@ -748,7 +756,7 @@ def tree_attention_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.
     B, Tmax, Hq, D = q.shape
     num_pages, Hkv, page_size, _ = k_pages.shape
     max_blocks = block_table.shape[1]
-    dt = {torch.float32: TSD_F32, torch.bfloat16: TSD_BF16}.get(q.dtype)
+    dt = _CODES.get(q.dtype)
     if dt is None:
         raise TypeError("q must be float32 or bfloat16")
     _need(q, "q", q.dtype, (B, Tmax, Hq, D), dev)
@@ -809,7 +817,7 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature: Optional[torch.Te
         raise ValueError("logits must be [R][V] and u [R][S]")
     R, V = logits.shape
     S = u.shape[1]
-    dt = {torch.float32: TSD_F32, torch.bfloat16: TSD_BF16}.get(logits.dtype)
+    dt = _CODES.get(logits.dtype)
     if dt is None:
         raise TypeError("logits must be float32 or bfloat16")
     ld = _need_matrix(logits, "logits", logits.dtype, (R, V), dev)
@@ -824,7 +832,8 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature: Optional[torch.Te
         _need(min_p, "min_p", torch.float32, (R,), dev)
     if tokens is None:
         tokens = torch.empty((R, S), dtype=torch.int32, device=dev)
-    _need(tokens, "tokens", torch.int32, (R, S), dev)
+    else:
+        _need(tokens, "tokens", torch.int32, (R, S), dev)
     if probs is None and with_probs:
         probs = torch.empty((R, V), dtype=torch.float32, device=dev)
     probs_ld = 0
@@ -833,9 +842,9 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature: Optional[torch.Te
         _apart(probs, "probs", logits)
     st = _status_for(dev, status)
     with _on(dev):
-        rc = lib.tsd_sample(_ptr(logits), ld, dt, R, V, _ptr(temperature), _ptr(top_k),
-                            _ptr(top_p), _ptr(min_p), _ptr(u), S, _ptr(tokens), _ptr(probs),
-                            probs_ld, _ptr(st), _stream(dev))
+        rc = lib.tsd_sample(logits.data_ptr(), ld, dt, R, V, _ptr(temperature), _ptr(top_k),
+                            _ptr(top_p), _ptr(min_p), u.data_ptr(), S, tokens.data_ptr(), _ptr(probs),
+                            probs_ld, st.data_ptr(), _stream(dev))
     _check(rc, "tsd_sample")
     return SampleResult(tokens, probs)
 
