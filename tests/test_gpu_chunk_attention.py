@@ -148,6 +148,12 @@ def test_ranges_over_many_blocks(cuda_device, dtype, B, Hkv, T, P):
     _check(_case(B + T, DTYPES[dtype], 2 * Hkv, Hkv, 64, 16, prefix, new, T, cuda_device))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Hq,T", [(130, 1), (130, 3), (256, 2)])
+def test_more_heads_than_a_block_has_rows(cuda_device, dtype, Hq, T):
+    _check(_case(Hq + T, DTYPES[dtype], Hq, 1, 64, 32, [100, 0, 40], [T, T, 1], T, cuda_device))
+
+
 def test_no_tokens_at_all(cuda_device):
     for dt in DTYPES.values():
         _check(_case(3, dt, 4, 2, 64, 16, [0, 33], [0, 0], 3, cuda_device))

@@ -117,7 +117,7 @@ const char *tsd_status_string(int status)
     }
 }
 
-int tsd_version(void) { return 101; }
+int tsd_version(void) { return 102; }
 
 unsigned long long tsd_launch_count(void) { return tsd::g_launches.load(); }
 

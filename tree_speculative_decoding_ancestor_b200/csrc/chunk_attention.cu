@@ -39,7 +39,7 @@ namespace {
 
 using namespace attn;
 
-constexpr int kMinTiles = 1;   // key tiles of a range at least
+constexpr int kMinTiles = 2;   // key tiles of a range at least
 
 struct Sizes {
     int B, Tmax, Hq, Hkv, Lmax, nrb;   // nrb: row blocks of the longest chunk
