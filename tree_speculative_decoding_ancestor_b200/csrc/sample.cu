@@ -18,7 +18,7 @@
 // into shared memory, and every later pass reads it there, a segment to each
 // warp.  Four CTAs of 256 threads share an SM: a search is a chain of short
 // dependent steps, and the others' passes fill its waits.  (1024 rows of 32000
-// with mixed settings: 286 us, 293 us as two CTAs of 512 threads, 450 to 650
+// with mixed settings: 280 us; 293 us as two CTAs of 512 threads, 450 to 650
 // us where the passes read the row from L2 instead and twice as many rows are
 // in flight.)
 //   1  the largest logit, and a bound below which no entry can be kept: the
@@ -161,8 +161,8 @@ struct Row {
         constexpr double kRound = 6755399441055744.0;   // 1.5 * 2^52
         constexpr double c1 = 0.6931471805599453 / 128.0, c2 = c1 * c1 / 2.0;
         constexpr double c3 = c1 * c2 / 3.0, c4 = c1 * c3 / 4.0;
-        double a = ((double)(deep ? x : fmaxf(x, low)) - top_d) * per_t;
-        if (deep)
+        double a = ((double)fmaxf(x, low) - top_d) * per_t;
+        if (deep)   // low is -inf
             a = fmax(a, -45.0 * 184.6649652337873);
         const double sum = a + kRound;
         const double r = a - (sum - kRound);
@@ -679,6 +679,7 @@ __global__ void __launch_bounds__(kThreads, 4)
     row.per_t = 184.6649652337873 / (double)T_;   // 128 / ln 2 / T
     row.low = hi - 45.f * T_;
     row.deep = !(fabs((double)hi - (double)row.low - 45.0 * (double)T_) <= (double)T_);
+    row.low = row.deep ? -INFINITY : row.low;
     row.step = (float)(kBins - 1) / fmaxf(fminf(hi - bound, kReach * T_), 1e-30f);
     const u64 floor_w = (u64)ceil((double)fminf(fmaxf(min_p, 0.f), 1.f) * scale);
 
@@ -783,13 +784,15 @@ __global__ void __launch_bounds__(kThreads, 4)
     if (min_p > 0.f)   // no logit below this one (with some margin) has weight min_p
         keep_from = fmaxf(keep_from, __double2float_rd((double)hi + (double)T_ *
                                                        (log((double)fminf(min_p, 1.f)) - 1e-3)));
+    // of the entries at keep_from itself those up to the threshold's token
+    const int last_tied =
+        threshold && keep_from == key_logit(threshold) ? (int)key_token(threshold) - first : a.V;
     auto kept4 = [&](int i, const float4 &x, u64 (&w)[4]) {
         const float e[4] = {x.x, x.y, x.z, x.w};
         bool keep[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            keep[j] = e[j] > keep_from || (e[j] == keep_from && e[j] > -INFINITY &&
-                                           order_key(e[j], row.first + i + j) >= threshold);
+            keep[j] = e[j] > keep_from || (e[j] == keep_from && i + j <= last_tied);
             w[j] = 0;
         }
         if (!__any_sync(0xffffffffu, keep[0] | keep[1] | keep[2] | keep[3]))
@@ -797,7 +800,12 @@ __global__ void __launch_bounds__(kThreads, 4)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const u64 v = row.weight(e[j], sh.table);
-            w[j] = keep[j] && v >= floor_w ? v : 0;
+            w[j] = keep[j] ? v : 0;
+        }
+        if (min_p > 0.f) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                w[j] = w[j] >= floor_w ? w[j] : 0;
         }
         return true;
     };
