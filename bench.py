@@ -369,6 +369,13 @@ def kernel_source_hash(text: str) -> str:
     return hashlib.sha256(text[i:j].encode()).hexdigest()[:16]
 
 
+def attention_source_hash(kernel_src: str) -> str:
+    """The kernels' section of the source file together with the header that
+    holds the parts they share with chunk attention."""
+    with open(kernel_src) as f, open(os.path.join(os.path.dirname(kernel_src), "attn_umma.cuh")) as g:
+        return hashlib.sha256((kernel_source_hash(f.read()) + g.read()).encode()).hexdigest()[:16]
+
+
 def _traffic_record(kernel_src: str, workload: str):
     """DRAM traffic of the dominant kernel from the committed ncu summary, if
     the summary was taken on the current source of the kernels."""
@@ -382,7 +389,7 @@ def _traffic_record(kernel_src: str, workload: str):
     if not rec:
         return None
     try:
-        h = kernel_source_hash(open(kernel_src).read())
+        h = attention_source_hash(kernel_src)
     except (ValueError, OSError):
         return None
     return rec.get("bytes_per_launch") if rec.get("kernel_sha") == h else None
