@@ -126,9 +126,10 @@ __device__ __forceinline__ float key_logit(u64 key)
 
 __device__ __forceinline__ uint32_t key_token(u64 key) { return 0xffffffffu - (uint32_t)key; }
 
-// The chunk of the row in shared memory, as this warp sees it.
-struct Row {
-    const float *l;       // the chunk (-inf behind its end, up to a multiple of four)
+// The chunk of the row in shared memory, in the logits' own type, as this warp
+// sees it.
+template <typename T> struct Row {
+    const T *l;           // the chunk (-inf behind its end, up to a multiple of four)
     int first;            // token id of its first logit
     int s0, s1;           // this warp's segment (s0 a multiple of four)
     int C, rank;
@@ -140,8 +141,13 @@ struct Row {
     // Logits i .. i + 3 (i a multiple of four); -inf beyond the segment.
     __device__ __forceinline__ float4 load(int i) const
     {
-        return i < s1 ? *reinterpret_cast<const float4 *>(l + i)
-                      : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (i >= s1)
+            return make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (sizeof(T) == 4)
+            return *reinterpret_cast<const float4 *>(l + i);
+        const uint2 v = *reinterpret_cast<const uint2 *>(l + i);   // bf16: the upper halves
+        return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u),
+                           __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
     }
     // f(i, x) for every four logits x at i of the segment; every lane takes
     // part in every call (i may be at or beyond s1).
@@ -389,7 +395,8 @@ __device__ __forceinline__ void list_in(Shared &sh, const float4 &x, int i, bool
 // The entry of step `bin` (found_count entries behind found_before and
 // found_before_mass) at which the limit is passed.  Returns its key, and in
 // mass_incl the mass up to and including it.
-__device__ __forceinline__ u64 resolve(Shared &sh, const Row &row, int bin, bool by_mass, u64 limit,
+template <typename T>
+__device__ __forceinline__ u64 resolve(Shared &sh, const Row<T> &row, int bin, bool by_mass, u64 limit,
                                     u64 *mass_incl)
 {
     const float from = (float)bin, to = (float)(bin + 1);
@@ -499,7 +506,8 @@ __device__ __forceinline__ u64 draw_at(double u, u64 total)
 // Step 2 behind the listing: n keys of the row, one per thread; the kept ones'
 // probabilities (over zeros) and the draws.  [first, last) are this CTA's
 // tokens, probs its part of the row.
-__device__ __forceinline__ void finish_list(Shared &sh, const SampleArgs &a, const Row &row, u64 key,
+template <typename T>
+__device__ __forceinline__ void finish_list(Shared &sh, const SampleArgs &a, const Row<T> &row, u64 key,
                                             int n, int top_k, float top_p, u64 floor_w, long long r,
                                             int first, int last, float *probs)
 {
@@ -552,10 +560,10 @@ __global__ void __launch_bounds__(kThreads, 4)
 {
     extern __shared__ float4 smem_raw[];
     Shared &sh = *reinterpret_cast<Shared *>(smem_raw);
-    float *const l = reinterpret_cast<float *>(smem_raw + (sizeof(Shared) + 15) / 16);
+    T *const l = reinterpret_cast<T *>(smem_raw + (sizeof(Shared) + 15) / 16);
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const long long r = blockIdx.x / C;
-    Row row;
+    Row<T> row;
     row.C = C;
     row.rank = (int)cluster_ctarank();
     row.l = l;
@@ -621,15 +629,14 @@ __global__ void __launch_bounds__(kThreads, 4)
             } x;
             x.raw = __ldg(reinterpret_cast<const uint4 *>(src) + i);
 #pragma unroll
-            for (int j = 0; j < N; j += 4)
-                *reinterpret_cast<float4 *>(l + i * N + j) =
-                    make_float4(clean(to_float(x.e[j])), clean(to_float(x.e[j + 1])),
-                                clean(to_float(x.e[j + 2])), clean(to_float(x.e[j + 3])));
+            for (int j = 0; j < N; ++j)
+                x.e[j] = from_float<T>(clean(to_float(x.e[j])));
+            *(reinterpret_cast<uint4 *>(l) + i) = x.raw;
         }
         done = nv * N;
     }
     for (int i = done + t; i < ((n_own + 3) & ~3); i += kThreads)
-        l[i] = i < n_own ? clean(to_float(src[i])) : -INFINITY;
+        l[i] = from_float<T>(i < n_own ? clean(to_float(src[i])) : -INFINITY);
     fill_exp_table(sh.table, scale);
     clear_hist(sh);
     if (t == 0)
@@ -669,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 4)
     }
     if (hi == INFINITY) {   // +inf stands for 0, everything else for -inf
         for (int i = t; i < ((n_own + 3) & ~3); i += kThreads)
-            l[i] = l[i] == INFINITY ? 0.f : -INFINITY;
+            l[i] = from_float<T>(to_float(l[i]) == INFINITY ? 0.f : -INFINITY);
         hi = 0.f;
         bound = -INFINITY;
         __syncthreads();
@@ -896,11 +903,12 @@ int sample_max_vocab() { return kMaxCluster * kMaxChunk; }
 
 int launch_sample(const SampleArgs &a, int R, int dtype, int num_sms, cudaStream_t stream)
 {
-    // CTAs per row: as few as hold the row at four CTAs per SM (8192 logits
+    // CTAs per row: as few as hold the row at four CTAs per SM (32 KB of logits
     // each, or what eight of them have to hold); more (down to 2048 logits
     // each) while the rows alone leave SMs idle.
+    const int es = dtype == TSD_BF16 ? 2 : 4;
     int C = 1;
-    while (C < kMaxCluster && ((a.V + C - 1) / C > 8192 ||
+    while (C < kMaxCluster && ((long long)(a.V + C - 1) / C * es > 32768 ||
                                ((long long)R * C < 2LL * num_sms && a.V / C >= 4096)))
         C *= 2;
     const int steps = (a.V + 127) / 128;
@@ -909,7 +917,7 @@ int launch_sample(const SampleArgs &a, int R, int dtype, int num_sms, cudaStream
     while ((1LL << log2v) < a.V)
         ++log2v;
     const int s = std::min(50, 63 - log2v);
-    const auto smem = [](int n) { return (sizeof(Shared) + 15) / 16 * 16 + (size_t)n * sizeof(float); };
+    const auto smem = [es](int n) { return (sizeof(Shared) + 15) / 16 * 16 + (size_t)n * es; };
     auto kern = dtype == TSD_BF16 ? sample_kernel<__nv_bfloat16> : sample_kernel<float>;
     constexpr int kMaxDevices = 64;
     static std::atomic<bool> raised[kMaxDevices][2];
