@@ -18,7 +18,7 @@
 // into shared memory, and every later pass reads it there, a segment to each
 // warp.  Four CTAs of 256 threads share an SM: a search is a chain of short
 // dependent steps, and the others' passes fill its waits.  (1024 rows of 32000
-// with mixed settings: 280 us; 293 us as two CTAs of 512 threads, 450 to 650
+// with mixed settings: 276 us; 293 us as two CTAs of 512 threads, 450 to 650
 // us where the passes read the row from L2 instead and twice as many rows are
 // in flight.)
 //   1  the largest logit, and a bound below which no entry can be kept: the
@@ -238,15 +238,15 @@ __device__ __forceinline__ void combine_and_scan(Shared &sh, int C, Scan &sc)
     sc.mass = 0;
     sc.count = 0;
 #pragma unroll 1
-    for (int r = 0; r < C; r += 2) {
-        uint32_t h[2][4];   // eight remote loads in flight
+    for (int r = 0; r < C; r += 4) {
+        uint32_t h[4][4];   // sixteen remote loads in flight
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 h[i][k] = r + i < C ? remote_u32(&sh.hist[k][t], r + i) : 0u;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
             sc.mass += (u64)h[i][1] + ((u64)h[i][2] << 16) + ((u64)h[i][3] << 32);
             sc.count += h[i][0];
         }
