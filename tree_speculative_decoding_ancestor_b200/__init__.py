@@ -1,6 +1,6 @@
 """B200-native verification hot path of tree speculative decoding (SpecInfer).
 
-Six operations, each a thin wrapper over the C ABI of ``lib/libtsd.so``
+The operations, each a thin wrapper over the C ABI of ``lib/libtsd.so``
 (``include/tsd.h``):
 
 * :func:`tree_mask_build`     -- ancestor bitmask / depth / child lists from ``parent[]``;
@@ -9,6 +9,11 @@ Six operations, each a thin wrapper over the C ABI of ``lib/libtsd.so``
 * :func:`tree_verify_greedy`  -- longest argmax-matching root path + one bonus token;
 * :func:`tree_verify_stochastic` -- multi-step speculative sampling (exact target distribution);
 * :func:`kv_commit`           -- move the accepted nodes' K/V rows after the prefix;
+* over a paged KV cache: :func:`rope_append_paged` (rotary positions of new tokens, appended
+  to the pages; :func:`rope_frequencies`), :func:`chunk_attention_paged` (causal attention of
+  prompt chunks and single tokens) and :func:`kv_commit_paged`;
+* :func:`sample`              -- tokens from filtered logits and given uniforms, with the
+  distribution they were drawn from (a row of ``q_probs``);
 * :func:`tree_expand`, :func:`tree_merge_chains`, :func:`tree_dfs_order` -- build the
   token tree (expansion top-k levels, merge of several SSMs' chains, depth-first order);
 * :func:`all_gather_accepted` -- with one batch per GPU, every rank's verification

@@ -529,7 +529,8 @@ __device__ __forceinline__ void finish_list(Shared &sh, const SampleArgs &a, con
     __syncthreads();
     const u64 total = sh.found_before_mass;
     const int token = (int)key_token(key);
-    if (probs && keep && token >= first && token < last)
+    if (probs && keep && token >= first && token < last &&
+        in_bounds(token, a.V, a.dev_status))
         probs[token - first] = (float)((double)w * (1.0 / (double)total));
     if (row.rank != 0 || a.S == 0)
         return;
@@ -550,7 +551,9 @@ __device__ __forceinline__ void finish_list(Shared &sh, const SampleArgs &a, con
             else
                 lo = mid + 1;
         }
-        a.tokens[r * a.S + s] = (int32_t)sh.swap[0][lo];
+        const int32_t drawn = (int32_t)sh.swap[0][lo];
+        if (in_bounds(drawn, a.V, a.dev_status))
+            a.tokens[r * a.S + s] = drawn;
     }
 }
 
@@ -887,7 +890,8 @@ __global__ void __launch_bounds__(kThreads, 4)
                     int j = 0;
                     while (j < 3 && m + w[j] <= at)
                         m += w[j++];
-                    a.tokens[r * a.S + s] = first + i + j;
+                    if (in_bounds(first + i + j, a.V, a.dev_status))
+                        a.tokens[r * a.S + s] = first + i + j;
                 }
                 break;
             }
