@@ -9,25 +9,29 @@
 // The rows of one KV head are packed r = t * G + g, so a block of BQ rows
 // reads each key once for all the query heads that share it, and its keys end
 // at the last row's position.  Two kernels:
-//   * bf16: tcgen05 products with S and O in TMEM (attn_umma.cuh), the
-//     geometry of tree attention: 128-key tiles at one CTA per SM, or, where a
-//     sequence's rows are one block of 128, 64-key tiles at two CTAs per SM
-//     (the KV stream is the bound there).  head_dim 64 or 128.
+//   * bf16: tcgen05 products with S and O in TMEM (attn_umma.cuh), 64-key tiles
+//     at two CTAs per SM: where the KV stream is the bound they keep twice the
+//     loads in flight, and in prompts one's products run beside the other's
+//     exponentials and its start and end (128-key tiles at one CTA per SM: 697
+//     against 603 us for 2048 tokens on 4096, 64/8 heads, two sequences; the
+//     same when the power limit paces both).  head_dim 64 or 128.
 //   * fp32: FMA tiles in registers (the tensor cores have no fp32 product).
 //
 // Work is divided in one of two ways.
-//   * Many blocks (prompts, large decode batches): one CTA per (block, KV head,
-//     sequence), the blocks with the most keys first.
-//   * Fewer blocks: the key tiles of all blocks in a row are cut into as many
-//     equal ranges as there are CTA slots, so every CTA streams the same number
-//     of tiles whatever the sequences' lengths, and its rings keep loading over
-//     the border from one block to the next.  A block that a border cuts leaves
+//   * Blocks: one CTA per (block, KV head, sequence), those with the most keys
+//     first.  Always taken from some number of blocks on (`chunk_plan`).
+//   * Ranges: the key tiles of all blocks in a row are cut into as many equal
+//     ranges as there are CTA slots, so every CTA streams the same number of
+//     tiles whatever the sequences' lengths, and its rings keep loading over the
+//     border from one block to the next.  A block that a border cuts leaves
 //     partial results, which a second kernel joins by their running maxima and
-//     sums.  The lengths are on the device: each warp of each CTA finds its
-//     range from them (a sum and a scan over at most some hundred items, no
-//     extra launch).  (Blocks split into pieces of about the same size, one CTA
-//     each: 75 to 98 us for 32 sequences of 512 to 4096 keys; pieces cannot be
-//     equal when lengths are not, and every CTA pays 4 us to start.)
+//     sums.
+// With few blocks the lengths decide, and they are on the device: each warp of
+// each CTA sums and scans them (some hundred items at most, no extra launch),
+// estimates both ways (`prefer_ranges`) and finds its share of the better one.
+// (Ranges against pieces of blocks, one CTA each: 63 against 75 to 98 us for 32
+// sequences of 512 to 4096 keys; pieces cannot be equal when lengths are not,
+// and every CTA pays 4 us to start.)
 #include <algorithm>
 #include <atomic>
 
@@ -43,9 +47,28 @@ constexpr int kMinTiles = 2;   // key tiles of a range at least
 
 struct Sizes {
     int B, Tmax, Hq, Hkv, Lmax, nrb;   // nrb: row blocks of the longest chunk
-    int ranges;                        // per KV head; 0: one CTA per block
+    int ranges;                        // per KV head; 0: blocks, whatever the lengths
     int part_rows;                     // rows of a partial result
+    float start, border, join;         // costs in key tiles, for prefer_ranges
 };
+
+// Whether ranges end sooner than blocks: `total` key tiles (of one KV head) in
+// `blocks` blocks, the longest of `longest`.  A range pays its tiles, a start,
+// one border per block, and the join; a block its tiles and a start, and what
+// more blocks than slots cost: about 0.6 of the longest at the end.  In tiles of
+// about 1 us (bf16), measured: 2 x 512 new tokens of 8/8 heads 15 us as blocks and 34
+// as ranges; 256 on 8192, 64/8 heads, 125 and 94; 40 single tokens on 2048 81 and 65,
+// on 64 to 512 18 and 28.
+__device__ __forceinline__ bool prefer_ranges(const Sizes &z, long long total, int blocks,
+                                              int longest)
+{
+    const float slots = (float)z.ranges, share = (float)total / slots;
+    const float busy = (float)blocks / slots;   // blocks per slot
+    const float as_ranges = share + z.start + z.border * busy + z.join;
+    const float as_blocks = busy <= 1.f ? (float)longest + 0.5f * z.start
+                                        : share + 0.6f * (float)longest + z.border * busy;
+    return as_ranges < as_blocks;
+}
 
 // Key tiles of block rb of a sequence; 0 for no rows (or a bad header).
 template <int BQ, int BN>
@@ -91,6 +114,25 @@ struct Walk {
         return block_tiles<BQ, BN>(z, rb, T, P);
     }
 
+    // This CTA's block; with `meta`, notes that there is nothing to join.
+    __device__ __forceinline__ bool begin_block(const Sizes &z, const int32_t *prefix_len,
+                                                const int32_t *chunk_len, int4 *meta)
+    {
+        const int pairs = z.B * z.Hkv, order = blockIdx.x / pairs, pair = blockIdx.x - order * pairs;
+        if (order >= z.nrb)
+            return false;
+        b = pair / z.Hkv;
+        hk = pair - b * z.Hkv;
+        item = b * z.nrb + z.nrb - 1 - order;   // most keys first
+        tile0 = 0;
+        n = load_item(z, prefix_len, chunk_len);
+        whole = true;
+        left = 0;
+        if (meta && (threadIdx.x & 31) == 0)
+            meta[item * z.Hkv + hk] = make_int4(0, 1, 0, 0);
+        return n > 0;
+    }
+
     // The first segment; false if the CTA has no work.  With `meta`, notes
     // where the pieces of every block that begins in this range will be.
     __device__ __forceinline__ bool begin(const Sizes &z, const int32_t *prefix_len,
@@ -98,21 +140,9 @@ struct Walk {
     {
         done = 0;
         slot = 0;
-        if (z.ranges == 0) {
-            const int pairs = z.B * z.Hkv, pair = blockIdx.x % pairs;
-            rb = z.nrb - 1 - blockIdx.x / pairs;   // most keys first
-            b = pair / z.Hkv;
-            hk = pair - b * z.Hkv;
-            item = b * z.nrb + rb;
-            tile0 = 0;
-            n = load_item(z, prefix_len, chunk_len);
-            whole = true;
-            left = 0;
-            return n > 0;
-        }
+        if (z.ranges == 0)
+            return begin_block(z, prefix_len, chunk_len, nullptr);
         const int lane = threadIdx.x & 31, items = z.B * z.nrb;
-        const int c = blockIdx.x / z.Hkv;
-        hk = blockIdx.x - c * z.Hkv;
         auto tiles_of = [&](int i) {
             const int s = i / z.nrb;
             return i < items ? block_tiles<BQ, BN>(z, i - s * z.nrb, chunk_len[s], prefix_len[s])
@@ -120,11 +150,23 @@ struct Walk {
         };
         const int tiles_first = tiles_of(lane);   // kept for the second pass
         long long total = tiles_first;
-        for (int i = lane + 32; i < items; i += 32)
-            total += tiles_of(i);
+        int longest = tiles_first, blocks = tiles_first > 0;
+        for (int i = lane + 32; i < items; i += 32) {
+            const int tiles = tiles_of(i);
+            total += tiles;
+            longest = max(longest, tiles);
+            blocks += tiles > 0;
+        }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
+        for (int o = 16; o > 0; o >>= 1) {
             total += __shfl_xor_sync(0xffffffffu, total, o);
+            longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+            blocks += __shfl_xor_sync(0xffffffffu, blocks, o);
+        }
+        if (!prefer_ranges(z, total, blocks, longest))
+            return begin_block(z, prefix_len, chunk_len, meta);
+        const int c = blockIdx.x / z.Hkv;
+        hk = blockIdx.x - c * z.Hkv;
         const long long ranges = min((long long)z.ranges, (total + kMinTiles - 1) / kMinTiles);
         if (c >= ranges)
             return false;
@@ -207,8 +249,7 @@ __device__ __forceinline__ void check_headers(const Sizes &z, const int32_t *pre
 }
 
 // ------------------------------------------------------------------- bf16
-template <int HD> using Wide = Geo<128, 3, 2, 512, HD>;
-template <int HD> using Half = Geo<64, 2, 2, 256, HD>;
+template <int HD> using Half = Geo<64, 2, 2, 256, HD>;   // 64-key tiles, two CTAs per SM
 
 // What a token's rows see: the keys in front of `end`; `all` of the block's
 // rows see those in front of the first row's end.
@@ -720,7 +761,6 @@ __global__ void __launch_bounds__(32 * kJoinRows)
 // -------------------------------------------------------------------- host
 struct Plan {
     Sizes z;
-    bool paired;        // bf16: 64-key tiles, two CTAs per SM
     int bq;
     long long grid;
     dim3 join;          // grid of the join
@@ -734,7 +774,6 @@ Plan chunk_plan(const ChunkArgs &a, int num_sms)
     const long long rows = (long long)a.Tmax * G;
     const bool f32 = a.dtype == TSD_F32;
     p.bq = f32 && rows > 16 ? 64 : f32 ? 16 : BQ;
-    p.paired = !f32 && rows <= BQ;
     p.z.B = a.B;
     p.z.Tmax = a.Tmax;
     p.z.Hq = a.Hq;
@@ -742,17 +781,27 @@ Plan chunk_plan(const ChunkArgs &a, int num_sms)
     p.z.Lmax = a.pages.max_blocks * a.pages.page_size;
     p.z.nrb = (int)((rows + p.bq - 1) / p.bq);
     p.z.part_rows = (int)std::min<long long>(rows, p.bq);
-    // CTA slots of the GPU.  Ranges of equal length while a slot would get fewer
-    // than four blocks (beyond that the blocks even out by themselves, and the
-    // few that end last cost less than partial results do).
-    const int slots = num_sms * (f32 || p.paired ? 2 : 1);
+    // in key tiles: of 1 us (bf16), 2 (fp32, 16 rows) and 5 (fp32, 64 rows);
+    // joining blocks of many rows costs more than a few rows
+    p.z.start = f32 ? (p.bq == 16 ? 5.f : 2.f) : 10.f;
+    p.z.border = 0.5f * p.z.start;
+    p.z.join = p.z.part_rows > 16 ? 1.5f * p.z.start : 0.f;
+    // CTA slots of the GPU.  From some number of blocks a slot they even out by
+    // themselves, and the few that end last cost less than partial results do:
+    // half a block where blocks are full (choosing and joining cost 5 us: 16/16
+    // heads, 2048 new tokens, 256 blocks, 53 without and 60 with), two where a
+    // sequence is one block (single tokens on 2048, 1024 blocks: 180 and 183;
+    // 320 blocks: 81 and 65), four for fp32
+    const int slots = num_sms * 2;
     const long long blocks = (long long)a.B * a.Hkv * p.z.nrb;
+    const long long most = f32 ? 4LL * slots : rows <= BQ ? 2LL * slots : slots / 2;
     size_t items = 0, parts = 0;
-    if (blocks < 4LL * slots) {
+    if (blocks < most) {
         p.z.ranges = std::max(slots / a.Hkv, 1);
-        p.grid = (long long)p.z.ranges * a.Hkv;
+        const long long cut = (long long)p.z.ranges * a.Hkv;
+        p.grid = std::max(cut, blocks);   // the lengths decide which of the two
         items = (size_t)a.B * p.z.nrb;
-        parts = (size_t)p.grid * 2;
+        parts = (size_t)cut * 2;
         p.join = dim3((unsigned)(items * a.Hkv), (p.z.part_rows + kJoinRows - 1) / kJoinRows);
     } else {
         p.z.ranges = 0;
@@ -792,8 +841,6 @@ cudaError_t set_smem_attributes()
         const void *kern;
         size_t bytes;
     } const all[] = {
-        {(const void *)chunk_attn_umma_kernel<Wide<128>, 3, 1>, Wide<128>::kSmemBytes},
-        {(const void *)chunk_attn_umma_kernel<Wide<64>, 3, 1>, Wide<64>::kSmemBytes},
         {(const void *)chunk_attn_umma_kernel<Half<128>, 2, 2>, Half<128>::kSmemBytes},
         {(const void *)chunk_attn_umma_kernel<Half<64>, 2, 2>, Half<64>::kSmemBytes},
         {(const void *)chunk_attn_fma_kernel<16, 64>, FmaSmem<16, 64>::kBytes},
@@ -813,15 +860,12 @@ int launch_umma(const ChunkArgs &a, const Plan &p, const Parts &parts, float sl2
                 cudaStream_t stream)
 {
     CUtensorMap tmK, tmV;
-    const int box = std::min(p.paired ? 64 : 128, a.pages.page_size);
+    const int box = std::min(Half<D>::BN, a.pages.page_size);
     const int planes = a.pages.num_pages * a.Hkv;
     if (!make_kv_map(&tmK, a.k, D, a.pages.page_size, planes, box) ||
         !make_kv_map(&tmV, a.v, D, a.pages.page_size, planes, box))
         return TSD_ERR_CUDA;
-    auto kern = p.paired ? chunk_attn_umma_kernel<Half<D>, 2, 2>
-                         : chunk_attn_umma_kernel<Wide<D>, 3, 1>;
-    const uint32_t smem = p.paired ? Half<D>::kSmemBytes : Wide<D>::kSmemBytes;
-    kern<<<(unsigned)p.grid, 192, smem, stream>>>(
+    chunk_attn_umma_kernel<Half<D>, 2, 2><<<(unsigned)p.grid, 192, Half<D>::kSmemBytes, stream>>>(
         tmK, tmV, static_cast<const __nv_bfloat16 *>(a.q), a.prefix_len, a.chunk_len, p.z, sl2,
         static_cast<__nv_bfloat16 *>(a.out), parts, a.dev_status, a.pages);
     TSD_LAUNCH_CHECK();
