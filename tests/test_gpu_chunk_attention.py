@@ -254,3 +254,25 @@ def test_lengths_on_the_device_may_change_between_replays(cuda_device):
         g.replay()
         fresh = _check((q, kp, vp, table, P, n))
         assert torch.equal(out, fresh)
+
+
+@pytest.mark.parametrize("dtype,Hq,Hkv,D,T", [("bf16", 4, 4, 64, 512), ("bf16", 16, 2, 128, 70),
+                                              ("f32", 4, 4, 64, 130)])
+def test_replays_with_lengths_that_change_how_work_is_divided(cuda_device, dtype, Hq, Hkv, D, T):
+    # short lengths are served block by block, a long one next to a short one by ranges
+    dev = cuda_device
+    q, kp, vp, table, P, n = _case(40 + T, DTYPES[dtype], Hq, Hkv, D, 64, [9000, 400], [T, T], T, dev,
+                                   poison=False)
+    assert tsd.chunk_attention_workspace_size(2, T, Hq, Hkv, D, 64, table.shape[1], DTYPES[dtype]) > 0
+    out = torch.zeros_like(q)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        tsd.chunk_attention_paged(q, kp, vp, table, P, n, out=out)
+    for p, m in (([0, 0], [T, T]), ([9000, 400], [T, 1]), ([0, 0], [T, 3]), ([9000, 0], [T // 2, T]),
+                 ([3, 1], [0, T]), ([0, 0], [0, 0])):
+        P.copy_(torch.tensor(p, dtype=torch.int32))
+        n.copy_(torch.tensor(m, dtype=torch.int32))
+        out.fill_(FILL)
+        g.replay()
+        fresh = _check((q, kp, vp, table, P, n))
+        assert torch.equal(out, fresh)
