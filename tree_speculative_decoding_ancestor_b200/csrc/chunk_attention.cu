@@ -13,7 +13,7 @@
 //     at two CTAs per SM: where the KV stream is the bound they keep twice the
 //     loads in flight, and in prompts one's products run beside the other's
 //     exponentials and its start and end (128-key tiles at one CTA per SM: 697
-//     against 603 us for 2048 tokens on 4096, 64/8 heads, two sequences; the
+//     against 611 us for 2048 tokens on 4096, 64/8 heads, two sequences; the
 //     same when the power limit paces both).  head_dim 64 or 128.
 //   * fp32: FMA tiles in registers (the tensor cores have no fp32 product).
 //
@@ -32,6 +32,7 @@
 // (Ranges against pieces of blocks, one CTA each: 63 against 75 to 98 us for 32
 // sequences of 512 to 4096 keys; pieces cannot be equal when lengths are not,
 // and every CTA pays 4 us to start.)
+
 #include <algorithm>
 #include <atomic>
 
@@ -789,7 +790,7 @@ Plan chunk_plan(const ChunkArgs &a, int num_sms)
     // CTA slots of the GPU.  From some number of blocks a slot they even out by
     // themselves, and the few that end last cost less than partial results do:
     // half a block where blocks are full (choosing and joining cost 5 us: 16/16
-    // heads, 2048 new tokens, 256 blocks, 53 without and 60 with), two where a
+    // heads, 2048 new tokens, 256 blocks, 51 without and 60 with), two where a
     // sequence is one block (single tokens on 2048, 1024 blocks: 180 and 183;
     // 320 blocks: 81 and 65), four for fp32
     const int slots = num_sms * 2;
