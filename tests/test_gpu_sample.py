@@ -251,3 +251,27 @@ def test_listed_and_searched_rows(cuda_device, k):
     logits, u = _logits(k, 6, 30011)
     _check(cuda_device, logits, u, k=[k] * 6, p=[1.0, 0.9, 0.5, 1.0, 0.99, 0.9], m=[0.0, 0.0, 0.0, 0.2,
                                                                                0.001, 0.05])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V,T", [(300, 1.0), (5000, 0.5), (100000, 1.0), (100000, 2.0)])
+def test_top_p_where_a_coarse_sum_misleads(cuda_device, V, T, dtype):
+    # weights that 2^-16 steps lose, or round up by half, beside a few large ones;
+    # limits in the large ones, in the body and far below
+    g = torch.Generator().manual_seed(V)
+    rows, p = [], []
+    for depth, mid, limits in ((13.0, 0, (0.5, 0.95, 0.9995, 0.99999)),
+                               (11.5, 8, (0.45, 0.56, 0.7, 0.9999)),
+                               (16.0, 3, (0.9, 0.9999))):
+        for limit in limits:
+            x = -depth + 1e-3 * torch.randn(V, generator=g)
+            at = torch.randperm(V, generator=g)[:mid + 1]
+            x[at] = -3.0 - 0.01 * torch.arange(mid + 1)
+            x[at[0]] = 0.0
+            rows.append(T * x + 5.0)
+            p.append(limit)
+    x = 4.0 * torch.randn(2, V, generator=g)
+    logits = torch.cat([torch.stack(rows), T * x]).to(dtype)
+    p += [0.9995, 0.99]
+    u = torch.rand(len(p), 3, generator=g, dtype=torch.float64)
+    _check(cuda_device, logits, u, T=[T] * len(p), p=p)

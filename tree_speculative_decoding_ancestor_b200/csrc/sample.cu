@@ -18,21 +18,27 @@
 // into shared memory, and every later pass reads it there, a segment to each
 // warp.  Four CTAs of 256 threads share an SM: a search is a chain of short
 // dependent steps, and the others' passes fill its waits.  (1024 rows of 32000
-// with mixed settings: 276 us; 293 us as two CTAs of 512 threads, 450 to 650
-// us where the passes read the row from L2 instead and twice as many rows are
-// in flight.)
-//   1  the largest logit, and a bound below which no entry can be kept: the
-//      threads' largest logits are sorted; the (top_k / C)-th of each CTA's
-//      256, the least of them over the cluster, has at least top_k entries at
-//      or above it, and not many more (top_p alone: the smallest of all, and
-//      the bound holds if the mass above it turns out to reach top_p)
+// with mixed settings: 259 us; before the guess of step 3, 276, and then 293 us
+// as two CTAs of 512 threads, 450 to 650 us where the passes read the row from
+// L2 instead and twice as many rows are in flight.)
+//   1  the largest logit, and with top_k a bound below which no entry can be
+//      kept: the threads' largest logits are sorted; the (top_k / C)-th of each
+//      CTA's 256, the least of them over the cluster, has at least top_k
+//      entries at or above it, and not many more
 //   2  the entries at or above the bound are listed (top_k = 50 of 32000: some
 //      60).  At most kList of them in the row: every CTA sorts them, and one
 //      scan of their weights answers top_k, top_p and min_p; sorted by token
 //      id, another scan answers the draws.  Otherwise:
 //   3  a histogram of the entries above the bound over 256 equal steps of the
 //      logit: count and mass per step, added up over the cluster; a scan finds
-//      the step in which the k-th entry, or the top_p mass, falls
+//      the step in which the k-th entry, or the top_p mass, falls.  For top_p
+//      alone the steps cover what a guess is worth: a histogram of fp32 weights
+//      (one add an entry instead of four) says about where the mass falls, and
+//      the exact masses above and below the steps around that are summed in
+//      registers.  If the limit is not among the steps after all, they are laid
+//      over the whole reach and the pass is repeated.  (1024 rows of 32000, top_p
+//      0.9 of twice normal logits: 308 us; 458 with steps over what the least of
+//      the threads' largest logits bounds, which is often short of top_p)
 //   4  that step's entries (usually some tens) are listed and sorted; the one
 //      at which the limit is passed is the threshold, as a 64-bit (logit,
 //      token id) key.  More than kList entries: the same histogram over the
@@ -63,6 +69,8 @@ constexpr int kListTop = kThreads / 2;  // top_k / C up to which listing is trie
 constexpr int kMaxCluster = 8;
 constexpr int kMaxChunk = 49152;        // logits of a CTA, 192 KB of shared memory
 constexpr float kReach = 40.f;          // e^-40 2^s < 1/2: weights from there on are 0
+constexpr int kGuessBins = 4 * kThreads;   // steps of the guess, four per thread
+constexpr float kGuessReach = 12.f;        // e^-12 2^16 < 1/2: guessed weights from there on are 0
 
 typedef unsigned long long u64;
 
@@ -77,12 +85,14 @@ struct Shared {
         u64 by_rank[kList];             // weights, then cumulative sums
     };
     u64 key[kList];                     // listed entries of this CTA
-    u64 swap[2][kThreads];              // of the sorts
-    u64 warp_sum[kWarps], scan_mass[kWarps];
-    uint32_t scan_count[kWarps];
+    union {
+        u64 swap[2][kThreads];          // of the sorts
+        uint4 guess[kThreads];          // guessed mass per step
+    };
+    u64 warp_sum[kWarps], warp_over[kWarps], scan_mass[kWarps];
     float warp_hi[kWarps];
     float hi, bound;                    // the CTA's largest logit and bound
-    u64 rest;                           // the CTA's mass below the bound
+    u64 over, rest;                     // the CTA's mass above and below the steps
     u64 key_hi, key_lo;                 // of the entries in question
     uint32_t listed;
     // the step (or entry) a search ended at
@@ -105,6 +115,16 @@ __device__ __forceinline__ uint32_t remote_u32(const void *p, uint32_t rank)
     uint32_t v;
     asm volatile("ld.shared::cluster.u32 %0, [%1];"
                  : "=r"(v)
+                 : "r"(cluster_map(xchg_smem_addr(p), rank))
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint4 remote_uint4(const void *p, uint32_t rank)
+{
+    uint4 v;
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "r"(cluster_map(xchg_smem_addr(p), rank))
                  : "memory");
     return v;
@@ -136,7 +156,7 @@ template <typename T> struct Row {
     bool deep;            // logits so large that top - 45 T is no float next to it
     float top, low;       // the row's largest logit, and one whose weight is 0
     double top_d, per_t;  // weight of x: 2^(((x - top) per_t) / 128)
-    float step;           // histogram steps per logit unit
+    float from, step;     // upper end of the histogram's steps, and steps per logit unit
 
     // Logits i .. i + 3 (i a multiple of four); -inf beyond the segment.
     __device__ __forceinline__ float4 load(int i) const
@@ -179,9 +199,9 @@ template <typename T> struct Row {
                                           __double2loint(fma(t, p, t)));
         return (u64)__double_as_longlong(y + 4503599627370496.0) & 0xfffffffffffffull;
     }
-    // Where x falls on the scale of histogram steps; kBins and above: out of
-    // reach, weight 0.
-    __device__ __forceinline__ float place(float x) const { return (top - x) * step; }
+    // Where x falls on the scale of histogram steps: below 0 above them, from
+    // kBins on below them (with the whole reach: weight 0).
+    __device__ __forceinline__ float place(float x) const { return (from - x) * step; }
 };
 
 __device__ __forceinline__ void mass_in(Shared &sh, int step, u64 w)
@@ -231,6 +251,7 @@ __device__ __forceinline__ u64 block_scan(Shared &sh, u64 v, u64 &total)
     return v;
 }
 
+// Peers may read this CTA's histogram until the next cluster barrier.
 __device__ __forceinline__ void combine_and_scan(Shared &sh, int C, Scan &sc)
 {
     const int t = threadIdx.x;
@@ -251,7 +272,6 @@ __device__ __forceinline__ void combine_and_scan(Shared &sh, int C, Scan &sc)
             sc.count += h[i][0];
         }
     }
-    cluster_sync_all();   // every CTA has read the histograms: they may be reused
     u64 total;
     sc.before_mass = block_scan(sh, sc.mass, total) - sc.mass;
     sc.before = (uint32_t)block_scan(sh, sc.count, total) - sc.count;
@@ -303,19 +323,12 @@ __device__ __forceinline__ u64 sort_descending(Shared &sh, u64 v, int n)
     return v;
 }
 
-// The q-th largest of the threads' values (a bitonic sort of them, unless it is
-// the smallest).  Begins behind the last readers of sh.swap.
+// The q-th largest of the threads' values (a bitonic sort of them).  Begins
+// behind the last readers of sh.swap.
 __device__ __forceinline__ float nth_largest(Shared &sh, float v, int q)
 {
     const int t = threadIdx.x;
     float *swap = reinterpret_cast<float *>(sh.swap);
-    if (q == kThreads) {
-        v = -warp_max(-v);
-        if ((t & 31) == 0)
-            swap[t >> 5] = v;
-        __syncthreads();
-        return -warp_max((t & 31) < kWarps ? -swap[t & 31] : -INFINITY);
-    }
     int buf = 0;
 #pragma unroll
     for (int size = 2; size <= kThreads; size <<= 1)
@@ -336,6 +349,58 @@ __device__ __forceinline__ float nth_largest(Shared &sh, float v, int q)
         swap[2 * kThreads] = v;
     __syncthreads();
     return swap[2 * kThreads];
+}
+
+// A guess at the step (of kGuessBins, of `unit` each, nearest one) in which
+// top_p of the row's sum is reached: weights in fp32, rounded to 2^-16 and added
+// up as integers (a chunk's are below 2^32), one atomic each.  Peers may read
+// sh.guess until the next cluster barrier.
+template <typename T>
+__device__ __forceinline__ int guess_step(Shared &sh, const Row<T> &row, float top_p, float unit)
+{
+    constexpr float kInt = 8388608.f;   // 2^23: x + 2^23 holds round(x) in its low bits
+    constexpr float kLog2 = -1.4426950408889634f * kGuessReach / kGuessBins;
+    uint32_t *const sums = &sh.guess[0].x;
+    const int t = threadIdx.x;
+    const float per = 1.f / unit;
+    row.walk([&](int, const float4 &x) {
+        const float e[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float f = (row.top - e[j]) * per;
+            if (f < kGuessBins - 1)
+                atomicAdd(&sums[__float_as_uint(f + kInt) & (kGuessBins - 1)],
+                          __float_as_uint(fmaf(exp2f(f * kLog2), 65536.f, kInt)) & 0x7fffffu);
+        }
+    });
+    cluster_sync_all();   // the sums are complete
+    u64 own[4] = {0, 0, 0, 0};   // of steps 4 t .. 4 t + 3
+#pragma unroll 1
+    for (int r = 0; r < row.C; r += 4) {
+        uint4 g[4];   // four remote loads in flight
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            g[i] = r + i < row.C ? remote_uint4(&sh.guess[t], r + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            own[0] += g[i].x;
+            own[1] += g[i].y;
+            own[2] += g[i].z;
+            own[3] += g[i].w;
+        }
+    }
+    const u64 all = own[0] + own[1] + own[2] + own[3];
+    u64 total;
+    u64 run = block_scan(sh, all, total) - all;
+    const u64 want = max((u64)1, (u64)(fmax((double)top_p, 0.0) * (double)total));
+    if (run < want && want <= run + all) {
+        int k = 0;
+        while (k < 3 && run + own[k] < want)
+            run += own[k++];
+        sh.found_bin = 4 * t + k;
+    }
+    __syncthreads();
+    return (int)sh.found_bin;
 }
 
 // Every CTA's listed keys, one per thread (0 beyond their number, n).  The
@@ -394,7 +459,8 @@ __device__ __forceinline__ void list_in(Shared &sh, const float4 &x, int i, bool
 
 // The entry of step `bin` (found_count entries behind found_before and
 // found_before_mass) at which the limit is passed.  Returns its key, and in
-// mass_incl the mass up to and including it.
+// mass_incl the mass up to and including it.  Peers may read this CTA's list
+// until the next cluster barrier.
 template <typename T>
 __device__ __forceinline__ u64 resolve(Shared &sh, const Row<T> &row, int bin, bool by_mass, u64 limit,
                                     u64 *mass_incl)
@@ -416,7 +482,7 @@ __device__ __forceinline__ u64 resolve(Shared &sh, const Row<T> &row, int bin, b
             sh.key_hi = 0;
             sh.key_lo = ~0ull;
         }
-        __syncthreads();
+        cluster_sync_all();   // and every CTA has read the last histogram
         u64 khi = 0, klo = ~0ull;
         row.walk([&](int i, const float4 &x) {
             const float e[4] = {x.x, x.y, x.z, x.w};
@@ -475,7 +541,7 @@ __device__ __forceinline__ u64 resolve(Shared &sh, const Row<T> &row, int bin, b
         sh.found_key = key;
         sh.found_mass = incl;
     }
-    cluster_sync_all();   // lists read everywhere; found_* complete here
+    __syncthreads();
     *mass_incl = sh.found_mass;
     const u64 key_found = sh.found_key;
     __syncthreads();
@@ -642,13 +708,15 @@ __global__ void __launch_bounds__(kThreads, 4)
         l[i] = from_float<T>(i < n_own ? clean(to_float(src[i])) : -INFINITY);
     fill_exp_table(sh.table, scale);
     clear_hist(sh);
+    if (top_k == 0)
+        sh.guess[t] = make_uint4(0, 0, 0, 0);
     if (t == 0)
         sh.listed = 0;
     // the bound: the q-th largest of the threads' largest logits, q such that
-    // C of these cover top_k; all threads' without top_k
-    const int q = top_k > 0 ? (top_k + C - 1) / C : kThreads;
+    // C of these cover top_k
+    const int q = (top_k + C - 1) / C;
     float bound = -INFINITY;
-    if (cut && q <= kThreads)
+    if (top_k > 0 && q <= kThreads)
         bound = nth_largest(sh, hi, q);
     hi = warp_max(hi);
     if (lane == 0)
@@ -690,12 +758,12 @@ __global__ void __launch_bounds__(kThreads, 4)
     row.low = hi - 45.f * T_;
     row.deep = !(fabs((double)hi - (double)row.low - 45.0 * (double)T_) <= (double)T_);
     row.low = row.deep ? -INFINITY : row.low;
+    row.from = hi;
     row.step = (float)(kBins - 1) / fmaxf(fminf(hi - bound, kReach * T_), 1e-30f);
     const u64 floor_w = (u64)ceil((double)fminf(fmaxf(min_p, 0.f), 1.f) * scale);
 
     // 2: few entries
-    bool some = bound > -INFINITY;
-    if (some && top_k > 0 && q <= kListTop) {
+    if (bound > -INFINITY && q <= kListTop) {
         row.walk([&](int i, const float4 &x) {
             list_in(sh, x, first + i, x.x >= bound, x.y >= bound, x.z >= bound, x.w >= bound);
         });
@@ -713,8 +781,16 @@ __global__ void __launch_bounds__(kThreads, 4)
     // 3, 4: the threshold
     const bool with_mass = top_p < 1.f, with_rest = with_mass && top_k == 0;
     u64 threshold = 0, total = 0;   // kept: keys from here up
+    bool guessed = with_rest;
+    if (guessed) {   // the steps: those around the guess, or everything below it near the reach
+        const float unit = fmaxf(kGuessReach * T_, 1e-30f) / kGuessBins;
+        const int g = guess_step(sh, row, top_p, unit);
+        row.from = g > 1 ? hi - ((float)g - 1.5f) * unit : hi;
+        const float to = g < kGuessBins - 3 ? hi - ((float)g + 1.5f) * unit : hi - kReach * T_;
+        row.step = (float)(kBins - 1) / fmaxf(row.from - to, 1e-30f);
+    }
     while (cut) {
-        u64 rest = 0;
+        u64 rest = 0, over = 0;
         row.walk([&](int i, const float4 &x) {
             const float e[4] = {x.x, x.y, x.z, x.w};
             u64 w[4] = {0, 0, 0, 0};
@@ -726,7 +802,9 @@ __global__ void __launch_bounds__(kThreads, 4)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float f = row.place(e[j]);
-                if (e[j] >= bound && f < (float)kBins) {
+                if (f < 0.f) {
+                    over += w[j];
+                } else if (e[j] >= bound && f < (float)kBins) {
                     count_in(sh, (int)f);
                     if (with_mass)
                         mass_in(sh, (int)f, with_rest ? w[j] : row.weight(e[j], sh.table));
@@ -737,17 +815,24 @@ __global__ void __launch_bounds__(kThreads, 4)
         });
         if (with_rest) {
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
+            for (int o = 16; o > 0; o >>= 1) {
+                over += __shfl_xor_sync(0xffffffffu, over, o);
                 rest += __shfl_xor_sync(0xffffffffu, rest, o);
-            if (lane == 0)
+            }
+            if (lane == 0) {
                 sh.warp_sum[warp] = rest;
+                sh.warp_over[warp] = over;
+            }
             __syncthreads();
             if (t == 0) {
-                rest = 0;
+                rest = over = 0;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w)
+                for (int w = 0; w < kWarps; ++w) {
                     rest += sh.warp_sum[w];
+                    over += sh.warp_over[w];
+                }
                 sh.rest = rest;
+                sh.over = over;
             }
         }
         Scan sc;
@@ -758,30 +843,38 @@ __global__ void __launch_bounds__(kThreads, 4)
         }
         if (with_rest) {
             rest = lane < C ? remote_u64(&sh.rest, lane) : 0;
+            over = lane < C ? remote_u64(&sh.over, lane) : 0;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
+            for (int o = 16; o > 0; o >>= 1) {
                 rest += __shfl_xor_sync(0xffffffffu, rest, o);
+                over += __shfl_xor_sync(0xffffffffu, over, o);
+            }
         }
         __syncthreads();
-        const u64 above = sh.found_mass;
+        const u64 within = sh.found_mass;
         const uint32_t entries = sh.found_count;
-        total = above + (with_rest ? rest : 0);
+        total = within + (with_rest ? over + rest : 0);
         __syncthreads();
         if (top_k > 0 && (uint32_t)top_k < entries) {
             find_step(sh, sc, false, (u64)top_k);
             threshold = resolve(sh, row, (int)sh.found_bin, false, (u64)top_k, &total);
+            if (with_mass)
+                cluster_sync_all();   // every CTA has read the list
         }
         if (with_mass) {
-            const u64 limit = mass_limit(top_p, total);
-            if (top_k == 0 && limit > above) {   // the mass above the bound is short of top_p
-                bound = -INFINITY;
+            const u64 limit = mass_limit(top_p, total) - (with_rest ? over : 0);
+            if (guessed && !(0 < (long long)limit && limit <= within)) {   // a wrong guess: all steps
+                guessed = false;
+                row.from = hi;
                 row.step = (float)(kBins - 1) / fmaxf(kReach * T_, 1e-30f);
+                cluster_sync_all();   // every CTA has read the others' sums
                 clear_hist(sh);
-                cluster_sync_all();   // and every CTA has read the others' rest
+                __syncthreads();
                 continue;
             }
             find_step(sh, sc, true, limit);
             threshold = resolve(sh, row, (int)sh.found_bin, true, limit, &total);
+            total += with_rest ? over : 0;
         }
         break;
     }
