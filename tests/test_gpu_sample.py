@@ -275,3 +275,28 @@ def test_top_p_where_a_coarse_sum_misleads(cuda_device, V, T, dtype):
     p += [0.9995, 0.99]
     u = torch.rand(len(p), 3, generator=g, dtype=torch.float64)
     _check(cuda_device, logits, u, T=[T] * len(p), p=p)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V,k", [(201, 150), (250, 129), (250, 200), (254, 253), (256, 150), (256, 255)])
+def test_rows_with_exactly_top_k_entries_above_the_bound(cuda_device, V, k, dtype):
+    # rows that start off a 16-byte boundary: a thread holds one entry, so the
+    # bound is the top_k-th largest itself; the other settings on top of it
+    logits, u = _logits(V + k, 8, V + 1, dtype)
+    _check(cuda_device, logits.to(cuda_device)[:, :V], u, T=[1.0, 0.7, 2.0, 1.0] * 2, k=[k] * 8,
+           p=[1.0, 1.0, 1.0, 0.9] * 2, m=[0.0, 0.0, 0.02, 0.0] * 2)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("R,C", [(2, 8), (300, 0)])
+def test_top_k_peaks_on_a_thread_each(cuda_device, R, C, dtype):
+    # 150 peaks in each chunk of a cluster, a 16-byte vector and so a thread
+    # each: top_k of them lie at or above the bound, and thousands below
+    V, each = 32000, 150
+    n = 128 // torch.finfo(dtype).bits
+    C = C or (4 if dtype == torch.float32 else 2)
+    logits, u = _logits(R, R, V, dtype, sigma=0.5)
+    starts = [V // 128 * r // C * 128 for r in range(C)]
+    peaks = torch.cat([s + n * torch.arange(each) for s in starts])
+    logits[:, peaks] = (5.0 + torch.rand(R, len(peaks))).to(dtype)
+    _check(cuda_device, logits, u, k=[C * each] * R)

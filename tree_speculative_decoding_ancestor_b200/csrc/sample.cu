@@ -855,7 +855,10 @@ __global__ void __launch_bounds__(kThreads, 4)
         const uint32_t entries = sh.found_count;
         total = within + (with_rest ? over + rest : 0);
         __syncthreads();
-        if (top_k > 0 && (uint32_t)top_k < entries) {
+        // (top_k entries or more lie at or above the bound, so with fewer inside the
+        // reach all that have weight are kept; with just as many the last of them is
+        // still the threshold, for others lie below the bound)
+        if (top_k > 0 && (uint32_t)top_k <= entries) {
             find_step(sh, sc, false, (u64)top_k);
             threshold = resolve(sh, row, (int)sh.found_bin, false, (u64)top_k, &total);
             if (with_mass)
