@@ -300,3 +300,14 @@ def test_top_k_peaks_on_a_thread_each(cuda_device, R, C, dtype):
     peaks = torch.cat([s + n * torch.arange(each) for s in starts])
     logits[:, peaks] = (5.0 + torch.rand(R, len(peaks))).to(dtype)
     _check(cuda_device, logits, u, k=[C * each] * R)
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,p", [(1.0, 1.0), (8.0, 1.0), (8.0, 0.9)])
+def test_entries_below_the_bound_in_its_step(cuda_device, T, p, dtype):
+    # the bound is 4, its step of the histogram also holds thousands at 3.95
+    V, n = 4000, 128 // torch.finfo(dtype).bits
+    logits = torch.full((2, V), 3.95)
+    logits[:, n * torch.arange(210)] = 4.0
+    logits[:, n * 255] = 30.0
+    u = torch.rand(2, 5, generator=torch.Generator().manual_seed(4), dtype=torch.float64)
+    _check(cuda_device, logits.to(dtype), u, T=[T] * 2, k=[200, 211], p=[p] * 2, exact=p == 1.0)

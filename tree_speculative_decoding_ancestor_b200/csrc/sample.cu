@@ -157,6 +157,7 @@ template <typename T> struct Row {
     float top, low;       // the row's largest logit, and one whose weight is 0
     double top_d, per_t;  // weight of x: 2^(((x - top) per_t) / 128)
     float from, step;     // upper end of the histogram's steps, and steps per logit unit
+    float bound;          // entries below it are in no step
 
     // Logits i .. i + 3 (i a multiple of four); -inf beyond the segment.
     __device__ __forceinline__ float4 load(int i) const
@@ -466,7 +467,8 @@ __device__ __forceinline__ u64 resolve(Shared &sh, const Row<T> &row, int bin, b
                                     u64 *mass_incl)
 {
     const float from = (float)bin, to = (float)(bin + 1);
-    u64 lo = 0, hi = ~0ull;   // keys in question
+    // keys in question: like the histogram, none below the bound
+    u64 lo = order_key(row.bound, 0xffffffffu), hi = ~0ull;
     auto in_question = [&](float x, int i) {
         const float f = row.place(x);
         if (!(f >= from && f < to))
@@ -760,6 +762,7 @@ __global__ void __launch_bounds__(kThreads, 4)
     row.low = row.deep ? -INFINITY : row.low;
     row.from = hi;
     row.step = (float)(kBins - 1) / fmaxf(fminf(hi - bound, kReach * T_), 1e-30f);
+    row.bound = bound;
     const u64 floor_w = (u64)ceil((double)fminf(fmaxf(min_p, 0.f), 1.f) * scale);
 
     // 2: few entries
