@@ -276,3 +276,22 @@ def test_replays_with_lengths_that_change_how_work_is_divided(cuda_device, dtype
         g.replay()
         fresh = _check((q, kp, vp, table, P, n))
         assert torch.equal(out, fresh)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("prefix", [[9000, 400], [10, 0]])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_query_row_that_is_not_a_number_shows(cuda_device, dtype, prefix, bad):
+    # whether its keys are served by one CTA or joined from pieces; inf - inf and
+    # inf * 0 are no numbers either; every other row as if it were not there
+    args = _case(50, DTYPES[dtype], 8, 2, 64, 64, prefix, [4, 2], 4, cuda_device, poison=False)
+    good = tsd.chunk_attention_paged(*args)
+    q = args[0].clone()
+    q[0, 1, 3, 5] = q[1, 0, 7, 0] = bad
+    out = tsd.chunk_attention_paged(q, *args[1:])
+    hit = torch.zeros(out.shape[:3], dtype=torch.bool, device=cuda_device)
+    hit[0, 1, 3] = hit[1, 0, 7] = True
+    assert torch.isnan(out[hit].float()).all()
+    for b, n in enumerate((4, 2)):
+        keep = ~hit[b, :n]
+        assert torch.equal(out[b, :n][keep], good[b, :n][keep])

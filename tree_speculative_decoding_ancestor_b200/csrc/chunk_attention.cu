@@ -686,8 +686,9 @@ __global__ void __launch_bounds__(kFmaThreads)
 
 // -------------------------------------------------------------------- join
 // One warp per row of a block that was cut: weights 2^(m_i - max m) over its
-// pieces (those of one range after the other), the weighted sum of their rows over the weighted sum
-// of their sums.  A piece none of whose keys the row sees has sum 0.
+// pieces (those of one range after the other), the weighted sum of their rows over
+// the weighted sum of their sums.  A piece none of whose keys the row sees has sum
+// 0; a sum that is no number (a q row with NaN) makes the row one.
 constexpr int kJoinRows = 8;   // rows (warps) of a CTA
 
 template <typename T, int D, int BQ_>
@@ -713,7 +714,7 @@ __global__ void __launch_bounds__(32 * kJoinRows)
     float M = -INFINITY;
     for (int i = lane; i < meta.y; i += 32) {
         const float2 ml = parts.ml[piece(i)];
-        M = fmaxf(M, ml.y > 0.f ? ml.x : -INFINITY);
+        M = fmaxf(M, ml.y == 0.f ? -INFINITY : ml.x);
     }
     M = warp_max(M);
     float acc[DL], L = 0.f;
@@ -724,7 +725,7 @@ __global__ void __launch_bounds__(32 * kJoinRows)
         float f = 0.f;   // lane's piece: its weight
         if (i0 + lane < meta.y) {
             const float2 ml = parts.ml[piece(i0 + lane)];
-            f = ml.y > 0.f ? exp2f(ml.x - M) : 0.f;
+            f = ml.y == 0.f ? 0.f : exp2f(ml.x - M);
             L = fmaf(f, ml.y, L);
         }
         const int n = min(32, meta.y - i0);
@@ -752,7 +753,7 @@ __global__ void __launch_bounds__(32 * kJoinRows)
     L = warp_sum(L);
     const int r = rb * BQ_ + lr;
     const size_t row = ((size_t)b * z.Tmax + r / G) * z.Hq + hk * G + r % G;
-    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const float inv = L == 0.f ? 0.f : 1.f / L;
     if (in_bounds((long long)row, (long long)z.B * z.Tmax * z.Hq, dev_status))
 #pragma unroll
         for (int k = 0; k < DL; ++k)
