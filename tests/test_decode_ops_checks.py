@@ -249,3 +249,14 @@ def test_rope_frequencies():
                 dict(rot_dim=64, scaling="other")):
         with pytest.raises(ValueError):
             tsd.rope_frequencies(**bad)
+
+
+@pytest.mark.parametrize("D,rows", [(128, 1), (128, 64)])
+def test_fp32_chunk_ranges_are_as_many_as_ctas_fit(D, rows):
+    # at head_dim 128 the fp32 tiles leave room for one CTA per SM: partial
+    # results for two blocks of each of them, and a page of indices and sums
+    L = tsd.load_library()
+    sms = torch.cuda.get_device_properties(0).multi_processor_count if torch.cuda.is_available() else 148
+    size = L.tsd_chunk_attention_workspace_size(1, rows, 1, 1, D, 16, 64, 0)
+    parts = 2 * sms * rows
+    assert parts * 4 * D <= size <= parts * (4 * D + 8) + 2 * 256 + 16

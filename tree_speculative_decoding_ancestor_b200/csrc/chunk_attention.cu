@@ -769,6 +769,21 @@ struct Plan {
     size_t meta_bytes, ml_bytes, o_bytes;
 };
 
+// CTAs of an SM: two, or the one that fits its 228 KB of shared memory (1 KB of
+// them reserved for each CTA): fp32 at head_dim 128.
+template <int BQ_, int D> constexpr int fma_ctas()
+{
+    return std::min<int>(2, (228 * 1024) / (FmaSmem<BQ_, D>::kBytes + 1024));
+}
+
+int ctas_per_sm(const ChunkArgs &a, int bq)
+{
+    if (a.dtype != TSD_F32)
+        return 2;
+    return a.D == 64 ? (bq == 16 ? fma_ctas<16, 64>() : fma_ctas<64, 64>())
+                     : (bq == 16 ? fma_ctas<16, 128>() : fma_ctas<64, 128>());
+}
+
 Plan chunk_plan(const ChunkArgs &a, int num_sms)
 {
     Plan p;
@@ -794,7 +809,7 @@ Plan chunk_plan(const ChunkArgs &a, int num_sms)
     // heads, 2048 new tokens, 256 blocks, 51 without and 60 with), two where a
     // sequence is one block (single tokens on 2048, 1024 blocks: 180 and 183;
     // 320 blocks: 81 and 65), four for fp32
-    const int slots = num_sms * 2;
+    const int slots = num_sms * ctas_per_sm(a, p.bq);
     const long long blocks = (long long)a.B * a.Hkv * p.z.nrb;
     const long long most = f32 ? 4LL * slots : rows <= BQ ? 2LL * slots : slots / 2;
     size_t items = 0, parts = 0;
