@@ -373,7 +373,8 @@ int tsd_kv_commit(void *k_cache, void *v_cache, const int32_t *prefix_len,
         return TSD_ERR_ALIGN;
     return tsd::launch_kv_commit(k_cache, v_cache, tsd::KvPages{}, prefix_len, out_path,
                                  n_accepted, B, Tmax, Hkv, Lmax, row_bytes, new_prefix_len,
-                                 dev_status, reinterpret_cast<cudaStream_t>(stream));
+                                 dev_status, device_sms(),
+                                 reinterpret_cast<cudaStream_t>(stream));
 }
 
 int tsd_kv_commit_paged(void *k_pages, void *v_pages, const int32_t *block_table, int num_pages,
@@ -401,7 +402,7 @@ int tsd_kv_commit_paged(void *k_pages, void *v_pages, const int32_t *block_table
     return tsd::launch_kv_commit(
         k_pages, v_pages, kv_pages(block_table, num_pages, page_size, max_blocks), prefix_len,
         out_path, n_accepted, B, Tmax, Hkv, max_blocks * page_size, row_bytes, new_prefix_len,
-        dev_status, reinterpret_cast<cudaStream_t>(stream));
+        dev_status, device_sms(), reinterpret_cast<cudaStream_t>(stream));
 }
 
 int tsd_rope_append_paged(const void *q, int64_t q_batch, int64_t q_token, const void *k,

@@ -114,14 +114,14 @@ __global__ void __launch_bounds__(kCommitThreads)
 int launch_kv_commit(void *k_cache, void *v_cache, const KvPages &pages,
                      const int32_t *prefix_len, const int32_t *out_path,
                      const int32_t *n_accepted, int B, int Tmax, int Hkv, int Lmax, int row_bytes,
-                     int32_t *new_prefix, int32_t *dev_status, cudaStream_t stream)
+                     int32_t *new_prefix, int32_t *dev_status, int num_sms, cudaStream_t stream)
 {
     if (B == 0)
         return TSD_OK;
     // KV heads of a CTA: one, and more while the CTAs would not fit the GPU at
-    // once (8 per SM of 148)
+    // once (8 per SM)
     int heads = 1;
-    while (heads < Hkv && (long long)B * ((Hkv + heads - 1) / heads) > 8 * 148)
+    while (heads < Hkv && (long long)B * ((Hkv + heads - 1) / heads) > 8LL * num_sms)
         heads *= 2;
     kv_commit_kernel<<<dim3((Hkv + heads - 1) / heads, B), kCommitThreads, 0, stream>>>(
         static_cast<uint4 *>(k_cache), static_cast<uint4 *>(v_cache), pages, prefix_len, out_path,

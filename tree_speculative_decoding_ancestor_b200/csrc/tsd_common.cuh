@@ -204,7 +204,7 @@ int launch_wait_probe(int kind, unsigned long long limit_ns, void *scratch,
 int launch_kv_commit(void *k_cache, void *v_cache, const KvPages &pages,
                      const int32_t *prefix_len, const int32_t *out_path,
                      const int32_t *n_accepted, int B, int Tmax, int Hkv, int Lmax, int row_bytes,
-                     int32_t *new_prefix, int32_t *dev_status, cudaStream_t stream);
+                     int32_t *new_prefix, int32_t *dev_status, int num_sms, cudaStream_t stream);
 
 struct RopeArgs {
     const void *q, *k, *v;
