@@ -260,3 +260,14 @@ def test_fp32_chunk_ranges_are_as_many_as_ctas_fit(D, rows):
     size = L.tsd_chunk_attention_workspace_size(1, rows, 1, 1, D, 16, 64, 0)
     parts = 2 * sms * rows
     assert parts * 4 * D <= size <= parts * (4 * D + 8) + 2 * 256 + 16
+
+
+def test_remembered_workspace_sizes_are_limited(lib):  # noqa: F811
+    q = torch.zeros(B, 1, Hq, D, **bf)
+    for blocks in range(1, 1200):   # a table that grows with the longest sequence
+        _chunk(q=q, block_table=torch.zeros(B, blocks, **i32))
+    info = binding._chunk_scratch.cache_info()
+    assert 0 < info.currsize <= info.maxsize <= 1024
+    n = len(lib.calls)
+    _chunk(q=q, block_table=torch.zeros(B, 1199, **i32))
+    assert not any(c.endswith("workspace_size") for c in lib.calls[n:])

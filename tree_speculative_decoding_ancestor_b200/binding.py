@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -535,15 +536,18 @@ def _pools(k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tens
     return num_pages, Hkv, page_size, max_blocks
 
 
-# Workspace bytes by (sizes, element type, device): they depend on nothing else.
-_chunk_scratch: Dict[Tuple, int] = {}
-
-
 def chunk_attention_workspace_size(B: int, Tmax: int, Hq: int, Hkv: int, D: int, page_size: int,
                                    max_blocks: int, dtype: torch.dtype) -> int:
     code = TSD_BF16 if dtype == torch.bfloat16 else TSD_F32
     return int(load_library().tsd_chunk_attention_workspace_size(B, Tmax, Hq, Hkv, D, page_size,
                                                                  max_blocks, code))
+
+
+@functools.lru_cache(maxsize=1024)
+def _chunk_scratch(sizes: Tuple[int, ...], device: Optional[int]) -> int:
+    """Workspace bytes for these sizes (element type included) on the current
+    device, `device`: they depend on nothing else."""
+    return int(load_library().tsd_chunk_attention_workspace_size(*sizes))
 
 
 def chunk_attention_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
@@ -579,11 +583,7 @@ def chunk_attention_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch
     st = _status_for(dev, status)
     sc = D ** -0.5 if scale is None else float(scale)
     with _on(dev):
-        sizes = (B, Tmax, Hq, Hkv, D, page_size, max_blocks, dt, dev.index)
-        need = _chunk_scratch.get(sizes)
-        if need is None:
-            need = int(lib.tsd_chunk_attention_workspace_size(*sizes[:-1]))
-            _chunk_scratch[sizes] = need
+        need = _chunk_scratch((B, Tmax, Hq, Hkv, D, page_size, max_blocks, dt), dev.index)
         ws = _scratch_for(dev, "chunk", need, workspace)
         rc = lib.tsd_chunk_attention_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
                                            block_table.data_ptr(), num_pages, page_size, max_blocks,
