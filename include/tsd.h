@@ -480,11 +480,11 @@ int tsd_kv_commit_paged(void *k_pages, void *v_pages, const int32_t *block_table
  * nor written.  q_out may not overlap q, k or v, and no two live slots may
  * share a cache row.  rot_dim is even and at most D; D * element size is a
  * multiple of 16 and at most 512 bytes; pointers and strides are multiples of
- * 16 bytes.  Host errors: TSD_ERR_NULL, TSD_ERR_SHAPE, TSD_ERR_DTYPE,
- * TSD_ERR_ALIGN, TSD_ERR_CUDA.  Device: TSD_DEV_BAD_PREFIX (n_new[b] outside
- * [0, Tmax], or P_b + n_new[b] outside the table's positions: nothing of that
- * sequence is written), TSD_DEV_BAD_PAGE (a block-table entry outside
- * [0, num_pages): that token's K and V rows are not written).
+ * 16 bytes; Tmax is at most 2^30.  Host errors: TSD_ERR_NULL, TSD_ERR_SHAPE,
+ * TSD_ERR_DTYPE, TSD_ERR_ALIGN, TSD_ERR_CUDA.  Device: TSD_DEV_BAD_PREFIX
+ * (n_new[b] outside [0, Tmax], or P_b + n_new[b] outside the table's positions:
+ * nothing of that sequence is written), TSD_DEV_BAD_PAGE (a block-table entry
+ * outside [0, num_pages): that token's K and V rows are not written).
  */
 int tsd_rope_append_paged(const void *q, int64_t q_batch, int64_t q_token, const void *k,
                           int64_t k_batch, int64_t k_token, const void *v, int64_t v_batch,

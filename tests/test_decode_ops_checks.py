@@ -271,3 +271,15 @@ def test_remembered_workspace_sizes_are_limited(lib):  # noqa: F811
     n = len(lib.calls)
     _chunk(q=q, block_table=torch.zeros(B, 1199, **i32))
     assert not any(c.endswith("workspace_size") for c in lib.calls[n:])
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="fake addresses must not reach a GPU")
+def test_c_rope_refuses_more_slots_than_positions():
+    # a grid of (Tmax + 3) / 4 CTAs: the sum would pass 31 bits
+    call = tsd.load_library().tsd_rope_append_paged
+    for Tmax in (2 ** 31 - 1, 2 ** 31 - 4, 2 ** 30 + 1):
+        assert call(_A, 256, 256, _A, 128, 128, _A, 128, 128, _A, 64, 0, 1.0, _A, _A, None, 2, Tmax, 4,
+                    2, 64, 1, _A, _A, _A, _A, 4, 16, 2, None, None) == -2
+    # as many as there can be positions get as far as the next check
+    assert call(None, 256, 256, _A, 128, 128, _A, 128, 128, _A, 64, 0, 1.0, _A, _A, None, 2, 2 ** 30, 4,
+                2, 64, 1, _A, _A, _A, _A, 4, 16, 2, None, None) == -1

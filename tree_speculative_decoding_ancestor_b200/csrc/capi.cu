@@ -415,8 +415,8 @@ int tsd_rope_append_paged(const void *q, int64_t q_batch, int64_t q_token, const
                           tsd_stream_t stream)
 {
     TSD_NVTX_RANGE();
-    if (B < 0 || B > kMaxGridY || Tmax < 1 || Hq < 1 || Hkv < 1 || Hq > (1 << 20) ||
-        Hkv > (1 << 20) || !page_sizes_ok(num_pages, page_size, max_blocks))
+    if (B < 0 || B > kMaxGridY || Tmax < 1 || Tmax > (1 << 30) || Hq < 1 || Hkv < 1 ||
+        Hq > (1 << 20) || Hkv > (1 << 20) || !page_sizes_ok(num_pages, page_size, max_blocks))
         return TSD_ERR_SHAPE;
     if (dtype != TSD_F32 && dtype != TSD_BF16)
         return TSD_ERR_DTYPE;
