@@ -384,3 +384,20 @@ def _run_keysplit(NSK, NSV, ntiles, seed, rescale_p=0.3):
 def test_keysplit_kernel_protocol(ntiles):
     for seed in range(150):
         _run_keysplit(3, 2, ntiles, seed)
+
+
+@pytest.mark.parametrize("slots", [2, 3])
+@pytest.mark.parametrize("issued", range(8))
+def test_waits_for_loads_in_flight_after_a_wait_that_gave_up(slots, issued):
+    """`drain` (csrc/attn_umma.cuh): with `issued` loads begun, and a load of a
+    slot begun only once the one before it there had been read, the parity waits
+    for phase i // slots of slot i % slots, i over the last `slots` loads, pass
+    exactly when all of them have landed."""
+    last = range(max(issued - slots, 0), issued)
+    for missing in [()] + [(i,) for i in last] + [tuple(last)]:
+        bars = [_Barrier(1) for _ in range(slots)]
+        for i in range(issued):
+            if i not in missing:
+                bars[i % slots].arrive()
+        passes = all((bars[i % slots].done & 1) != ((i // slots) & 1) for i in last)
+        assert passes == (not missing)

@@ -42,7 +42,7 @@ struct Geo {
     static constexpr uint32_t kOffK = kOffQ + kTileQ;
     static constexpr uint32_t kOffV = kOffK + NSK * kTile;
     static constexpr uint32_t kOffBar = kOffV + NSV * kTile;
-    static constexpr int kNumBars = 1 + 2 * NSK + 2 * NSV + 16;
+    static constexpr int kNumBars = 1 + 2 * NSK + 2 * NSV + 18;
     static constexpr uint32_t kOffMisc = kOffBar + 8 * kNumBars;
     static constexpr uint32_t kOffXchg = kOffMisc + 16;    // the softmax pairs' exchange slots
     static constexpr uint32_t kXchgBytes = 4 * 528;        // 4 x sizeof(PairXchg)
@@ -52,8 +52,8 @@ struct Geo {
 };
 
 // mbarrier addresses: q_full, k_full[NSK], k_empty[NSK], v_full[NSV],
-// v_empty[NSV], s_full[4], p_full[4], o_ready[4], pair[4] -- consecutive
-// 8-byte words.
+// v_empty[NSV], s_full[4], p_full[4], o_ready[4], pair[4], drained (and one
+// unused) -- consecutive 8-byte words.
 template <class Gm>
 struct Bars {
     static constexpr int NSK = Gm::NSK, NSV = Gm::NSV;
@@ -68,6 +68,8 @@ struct Bars {
     __device__ uint32_t o_ready(int i) const { return base + 8u * (9 + 2 * NSK + 2 * NSV + i); }
     // the two softmax warps of TMEM lane quarter i meet here (two arrivals)
     __device__ uint32_t pair(int i) const { return base + 8u * (13 + 2 * NSK + 2 * NSV + i); }
+    // only after a wait that gave up: every product issued is done
+    __device__ uint32_t drained() const { return base + 8u * (17 + 2 * NSK + 2 * NSV); }
 };
 
 // A wait whose outcome is the same on every lane of the warp (the TMEM
@@ -129,6 +131,7 @@ struct Setup {
     uint32_t base, sQ, sK, sV, tmem;
     Bars<Gm> bars;
     volatile int *abort_flag;
+    volatile int *loads;   // K and V tiles the producer has issued, once it is done
 };
 
 template <class Gm>
@@ -147,6 +150,7 @@ __device__ __forceinline__ Setup<Gm> cta_setup(uint8_t *smem_raw, uint32_t q_arr
     su.bars = Bars<Gm>{su.base + Gm::kOffBar};
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(su.gbase + kOffMisc);
     su.abort_flag = reinterpret_cast<volatile int *>(su.gbase + kOffMisc + 4);
+    su.loads = reinterpret_cast<volatile int *>(su.gbase + kOffMisc + 8);
     if (threadIdx.x == 0) {
         ptx::mbar_init(su.bars.q_full(), q_arrivals);
         for (int i = 0; i < NSK; ++i) {
@@ -163,6 +167,7 @@ __device__ __forceinline__ Setup<Gm> cta_setup(uint8_t *smem_raw, uint32_t q_arr
             ptx::mbar_init(su.bars.p_full(i), p_arrivals);
             ptx::mbar_init(su.bars.pair(i), 2);
         }
+        ptx::mbar_init(su.bars.drained(), 1);
         *su.abort_flag = 0;
         ptx::fence_barrier_init();
         ptx::fence_proxy_async_smem();
@@ -178,14 +183,43 @@ __device__ __forceinline__ Setup<Gm> cta_setup(uint8_t *smem_raw, uint32_t q_arr
     return su;
 }
 
+// After a wait that gave up: what this CTA still has in flight -- the products
+// issued by this thread (the MMA warp's lane 0), and the last load of every ring
+// slot -- lands before its shared memory and TMEM are given back.  Load i of a
+// ring of n slots is phase i / n of slot i % n, and no later one was begun.  Each
+// wait ends after 100 ms at the latest.
+template <class Gm>
+__device__ __forceinline__ void drain(const Setup<Gm> &su)
+{
+    const uint64_t t0 = ptx::global_timer_ns();
+    auto landed = [&](uint32_t bar, int phase) {
+        while (!ptx::mbar_try_wait(bar, phase & 1) &&
+               ptx::global_timer_ns() - t0 <= 100000000ull) {
+        }
+    };
+    ptx::mma_commit(su.bars.drained());
+    landed(su.bars.drained(), 0);
+    const int nk = su.loads[0], nv = su.loads[1];
+    for (int i = max(nk - Gm::NSK, 0); i < nk; ++i)
+        landed(su.bars.k_full(i % Gm::NSK), i / Gm::NSK);
+    for (int i = max(nv - Gm::NSV, 0); i < nv; ++i)
+        landed(su.bars.v_full(i % Gm::NSV), i / Gm::NSV);
+}
+
 template <class Gm>
 __device__ __forceinline__ void cta_teardown(const Setup<Gm> &su, int32_t *dev_status)
 {
     ptx::tc_fence_before();
     __syncthreads();
-    if (*su.abort_flag && threadIdx.x == 0)
+    const bool gave_up = *su.abort_flag != 0;
+    if (gave_up && threadIdx.x == 0)
         flag(dev_status, TSD_DEV_TIMEOUT);
     if ((threadIdx.x >> 5) == 1) {
+        if (gave_up) {
+            if ((threadIdx.x & 31) == 0)
+                drain(su);
+            __syncwarp();
+        }
         ptx::tc_fence_after();
         ptx::tmem_dealloc(su.tmem, Gm::kTmemCols);
     }
@@ -322,6 +356,8 @@ __device__ __forceinline__ void produce_kv(const Setup<Gm> &su, const CUtensorMa
             ++j;
         }
     }
+    su.loads[0] = i;
+    su.loads[1] = j;
 }
 
 // MMA warp, S = Q K^T for key tile `t` into TMEM columns `col_s`.

@@ -316,11 +316,12 @@ __device__ __forceinline__ void produce_range(const Setup<Gm> &su, const CUtenso
     }
     bool more_k = true, more_v = true;
     int page_k = entry(wk, 0);
-    for (int i = 0, j = 0; more_k || more_v;) {   // next K tile, next V tile of the range
+    int i = 0, j = 0;   // next K tile, next V tile of the range
+    while (more_k || more_v) {
         if (more_k && (!more_v || i < NSK || (j >= NSV && i <= j - 1 + kLead))) {
             const int s = i % NSK;
             if (i >= NSK && !warp_wait(su.bars.s_full(s), ((i / NSK) - 1) & 1, su.abort_flag))
-                return;
+                break;
             load(su.sK + s * Gm::kTile, tmK, su.bars.k_full(s), wk, jk, page_k);
             ++i;
             if (++jk == wk.n) {
@@ -332,7 +333,7 @@ __device__ __forceinline__ void produce_range(const Setup<Gm> &su, const CUtenso
         } else {
             const int s = j % NSV, r = j - NSV;   // PV_r read this slot last
             if (j >= NSV && !warp_wait(su.bars.o_ready(r % NS), (r / NS) & 1, su.abort_flag))
-                return;
+                break;
             load(su.sV + s * Gm::kTile, tmV, su.bars.v_full(s), wv, jv, entry(wv, jv));
             ++j;
             if (++jv == wv.n) {
@@ -340,6 +341,10 @@ __device__ __forceinline__ void produce_range(const Setup<Gm> &su, const CUtenso
                 more_v = wv.next(z, prefix_len, chunk_len);
             }
         }
+    }
+    if (lane == 0) {
+        su.loads[0] = i;
+        su.loads[1] = j;
     }
 }
 
