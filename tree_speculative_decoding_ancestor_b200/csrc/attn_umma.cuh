@@ -225,13 +225,6 @@ __device__ __forceinline__ void cta_teardown(const Setup<Gm> &su, int32_t *dev_s
     }
 }
 
-// The TMA loads of one [BN keys][128] K or V tile starting at logical key
-// position pos0 into `dst` (two 64-column halves).  Contiguous cache: one box
-// per half at (x, pos0, b * Hkv + hk).  Paged cache: one box per page the
-// tile touches (box rows = min(BN, page_size); a box never straddles a page
-// since both are powers of two and pos0 is a multiple of BN) at (x, row in
-// page, page * Hkv + hk).  A box that starts at or beyond the sequence's end
-// loads any valid page: those keys are masked and their V rows zeroed.
 // The block-table entries of the pages a CTA's key range [kb, seq_end)
 // touches, staged in shared memory by the producer warp before its first
 // load (at most kTableCache of them; entries past that are read from global
@@ -257,6 +250,13 @@ __device__ __forceinline__ PageCache stage_pages(const Setup<Gm> &su, const KvPa
     return pc;
 }
 
+// The TMA loads of one [BN keys][128] K or V tile starting at logical key
+// position pos0 into `dst` (two 64-column halves).  Contiguous cache: one box
+// per half at (x, pos0, b * Hkv + hk).  Paged cache: one box per page the
+// tile touches (box rows = min(BN, page_size); a box never straddles a page
+// since both are powers of two and pos0 is a multiple of BN) at (x, row in
+// page, page * Hkv + hk).  A box that starts at or beyond the sequence's end
+// loads any valid page: those keys are masked and their V rows zeroed.
 template <class Gm>
 __device__ __forceinline__ void load_kv_tile(uint32_t dst, const CUtensorMap *tm, uint32_t bar,
                                              int pos0, int b, int hk, int Hkv,
@@ -382,10 +382,6 @@ __device__ __forceinline__ void issue_qk(const Setup<Gm> &su, int lane, uint32_t
         __syncwarp();
 }
 
-// MMA warp, O += P V for key tile `t` (P in TMEM columns col_p); zeroes the
-// V rows at or beyond P_b + T_b first.  P_SPLIT: the packed P of keys
-// 64 .. 127 sits 64 columns after that of keys 0 .. 63 (each softmax half
-// writes into its own score columns) instead of right after it.
 // Zero the rows first_bad .. BN-1 of V ring slot vs (cache rows at or beyond
 // P_b + T_b: masked keys whose P is 0, but 0 * NaN would not be), by one warp,
 // then make the generic-proxy stores visible to the tensor cores.
@@ -403,6 +399,10 @@ __device__ __forceinline__ void zero_v_rows(const Setup<Gm> &su, int vs, int fir
     __syncwarp();
 }
 
+// MMA warp, O += P V for key tile `t` (P in TMEM columns col_p); zeroes the
+// V rows at or beyond P_b + T_b first.  P_SPLIT: the packed P of keys
+// 64 .. 127 sits 64 columns after that of keys 0 .. 63 (each softmax half
+// writes into its own score columns) instead of right after it.
 template <class Gm, bool RING_COMMIT = true, bool P_SPLIT = false, bool COMMIT = true,
           bool ZERO = true>
 __device__ __forceinline__ void issue_pv(const Setup<Gm> &su, int lane, uint32_t col_p,
