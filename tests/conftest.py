@@ -19,3 +19,16 @@ def cuda_device():
     if not torch.cuda.is_available():
         pytest.skip("no CUDA device")
     return torch.device("cuda:0")
+
+
+@pytest.fixture(autouse=True)
+def bounds_flag_stays_clear(request):
+    """On the bounds-checked build a GPU test also fails if one of its calls
+    that left the status word to the binding computed an index outside a
+    buffer (calls with a status word of their own assert on that)."""
+    yield
+    if request.node.get_closest_marker("gpu") is None:
+        return
+    from tree_speculative_decoding_ancestor_b200 import binding
+    for word in binding._status.values():
+        assert not int(word.item()) & binding.DEV_BOUNDS

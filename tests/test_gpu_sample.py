@@ -301,6 +301,7 @@ def test_top_k_peaks_on_a_thread_each(cuda_device, R, C, dtype):
     logits[:, peaks] = (5.0 + torch.rand(R, len(peaks))).to(dtype)
     _check(cuda_device, logits, u, k=[C * each] * R)
 
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("T,p", [(1.0, 1.0), (8.0, 1.0), (8.0, 0.9)])
 def test_entries_below_the_bound_in_its_step(cuda_device, T, p, dtype):

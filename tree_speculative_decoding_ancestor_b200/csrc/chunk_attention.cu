@@ -234,6 +234,11 @@ struct Walk {
     {
         return (size_t)(2 * blockIdx.x + slot) * z.part_rows + r;
     }
+    // checked build: the row is one of the partial results'
+    __device__ __forceinline__ bool part_ok(const Sizes &z, size_t at, int32_t *dev_status) const
+    {
+        return in_bounds((long long)at, 2LL * z.ranges * z.Hkv * z.part_rows, dev_status);
+    }
 };
 
 // A malformed header is reported by the first CTA that can see it.
@@ -473,7 +478,8 @@ __global__ void __launch_bounds__(192, kMinBlocks)
                     write_row<HD>(taddr_o, inv, row_ok, row, 1, 0, 0, out, nullptr, 0, HD);
                 } else {
                     const size_t at = w.part_row(z, tr);
-                    const bool keep = row_ok && tr < z.part_rows;
+                    const bool keep =
+                        row_ok && tr < z.part_rows && w.part_ok(z, at, dev_status);
                     write_row<HD>(taddr_o, 1.f, keep, at, 2, 0, 0, out, parts.o, 0, HD);
                     if (keep)
                         parts.ml[at] = make_float2(m_run, l_run);
@@ -677,6 +683,8 @@ __global__ void __launch_bounds__(kFmaThreads)
                                            dev_status))
                 continue;
             const size_t at = w.part_row(z, lr);
+            if (!w.whole && !w.part_ok(z, at, dev_status))
+                continue;
             float *dst = w.whole ? out + out_row(lr) * D : parts.o + at * D;
             const float f = w.whole ? (l[a] > 0.f ? 1.f / l[a] : 0.f) : 1.f;
 #pragma unroll

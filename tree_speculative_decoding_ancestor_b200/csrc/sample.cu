@@ -664,13 +664,14 @@ __global__ void __launch_bounds__(kThreads, 4)
     const bool probs_vec = (reinterpret_cast<uintptr_t>(probs) & 15u) == 0;
     auto put4 = [&](int i, float p0, float p1, float p2, float p3) {
         if (probs_vec && i + 3 < row.s1) {
-            *reinterpret_cast<float4 *>(probs + i) = make_float4(p0, p1, p2, p3);
+            if (in_bounds(first + i + 3, a.V, a.dev_status))
+                *reinterpret_cast<float4 *>(probs + i) = make_float4(p0, p1, p2, p3);
             return;
         }
         const float p[4] = {p0, p1, p2, p3};
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (i + j < row.s1)
+            if (i + j < row.s1 && in_bounds(first + i + j, a.V, a.dev_status))
                 probs[i + j] = p[j];
     };
     auto zeros = [&]() {
@@ -689,11 +690,18 @@ __global__ void __launch_bounds__(kThreads, 4)
         return x;
     };
     constexpr int N = 16 / sizeof(T);
+    const int room = (steps + C - 1) / C * 128;   // logits that the chunk may hold
+    auto fits = [&](int i, int n) {   // logits i .. i + n - 1 of the chunk
+        return in_bounds(i + n - 1, room, a.dev_status) &&
+               in_bounds(first + i + n - 1, a.V, a.dev_status);
+    };
     int done = 0;
     if ((reinterpret_cast<uintptr_t>(src) & 15u) == 0) {   // whole 16-byte vectors
         const int nv = n_own / N;
 #pragma unroll 4
         for (int i = t; i < nv; i += kThreads) {
+            if (!fits(i * N, N))
+                continue;
             union {
                 uint4 raw;
                 T e[N];
@@ -707,7 +715,8 @@ __global__ void __launch_bounds__(kThreads, 4)
         done = nv * N;
     }
     for (int i = done + t; i < ((n_own + 3) & ~3); i += kThreads)
-        l[i] = from_float<T>(i < n_own ? clean(to_float(src[i])) : -INFINITY);
+        if (i < n_own ? fits(i, 1) : in_bounds(i, room, a.dev_status))
+            l[i] = from_float<T>(i < n_own ? clean(to_float(src[i])) : -INFINITY);
     fill_exp_table(sh.table, scale);
     clear_hist(sh);
     if (top_k == 0)
