@@ -231,8 +231,9 @@ int tsd_tree_attention_paged(const void *q, const void *k_pages, const void *v_p
  * 0 < scale <= 1e30.  Keys at or beyond P_b + T_b never reach a result,
  * whatever the cache holds there; the K and V rows in front of it are finite
  * numbers (a V row that is not reaches also the tokens of its chunk in front
- * of it, as 0 * inf does).  Pointers 16-byte aligned; B at most 65535,
- * B * Hkv at most 2^24, Tmax * Hq / Hkv at most 2^30.
+ * of it, as 0 * inf does).  A q row that holds NaN gives a row of NaN.
+ * Pointers 16-byte aligned; B at most 65535, B * Hkv at most 2^24, Tmax * Hq /
+ * Hkv at most 2^30.
  * Host errors: TSD_ERR_NULL, TSD_ERR_SHAPE, TSD_ERR_DTYPE, TSD_ERR_ALIGN,
  * TSD_ERR_WORKSPACE, TSD_ERR_CUDA.  Device: TSD_DEV_BAD_PREFIX (T_b outside
  * [0, Tmax] or P_b + T_b outside the table: that sequence's rows are not

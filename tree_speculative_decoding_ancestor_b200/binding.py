@@ -187,7 +187,9 @@ _workspace: Dict[Tuple[int, str, int], torch.Tensor] = {}
 
 
 def device_status(device=None) -> torch.Tensor:
-    """The int32 word that the kernels OR their TSD_DEV_* bits into."""
+    """The int32 word that the kernels OR their TSD_DEV_* bits into.  It is made by
+    its first use on a device: ask for it, or make a call, before capturing a
+    graph (made within a capture, its zeroing would be replayed with the graph)."""
     device = torch.device(device or torch.cuda.current_device())
     idx = device.index if device.index is not None else torch.cuda.current_device()
     if idx not in _status:

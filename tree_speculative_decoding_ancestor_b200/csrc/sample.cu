@@ -48,7 +48,9 @@
 //   5  the probabilities, and the kept sums of each warp's segment; from them
 //      each draw's segment, which its warp walks
 // Bound: the read of the logits and the write of the probabilities; for rows
-// cut by top_p alone, or not at all, the exponentials of all entries.
+// cut by top_p alone, or not at all, the exponentials of all entries; the chain of
+// a search's steps.  Rows off a 16-byte boundary (most rows of an odd vocabulary) are
+// loaded and stored element by element: 1024 rows of 50257 fp32 498 us, of 50304 467.
 #include <algorithm>
 #include <atomic>
 
