@@ -283,3 +283,17 @@ def test_c_rope_refuses_more_slots_than_positions():
     # as many as there can be positions get as far as the next check
     assert call(None, 256, 256, _A, 128, 128, _A, 128, 128, _A, 64, 0, 1.0, _A, _A, None, 2, 2 ** 30, 4,
                 2, 64, 1, _A, _A, _A, _A, 4, 16, 2, None, None) == -1
+
+
+@pytest.mark.parametrize("kind", ["attn", "verify", "chunk"])
+def test_captured_calls_of_every_kind_own_their_workspace(lib, monkeypatch, kind):  # noqa: F811
+    # a graph outlives the cache's buffer, which a larger call replaces
+    real = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, device=None, **kw: real(*a, **kw))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    monkeypatch.setattr(binding, "_workspace", {})
+    dev = torch.device("cuda", 0)
+    get = binding._scratch_for if kind == "chunk" else binding._workspace_for
+    a, b = (get(dev, kind, 512, None) for _ in range(2))
+    assert a.numel() >= 512 and b.numel() >= 512 and a.data_ptr() != b.data_ptr()
+    assert binding._workspace == {}

@@ -214,8 +214,13 @@ def _get_workspace(device: torch.device, kind: str, nbytes: int) -> torch.Tensor
 def _workspace_for(device: torch.device, kind: str, nbytes: int,
                    workspace: Optional[torch.Tensor]) -> torch.Tensor:
     """The caller's workspace (a contiguous uint8 tensor on the device: its
-    element count is the byte count the library checks), or the cache's."""
+    element count is the byte count the library checks), or the cache's.  A
+    call that is being captured gets a buffer of its own instead: it belongs to
+    the graph, so that two graphs never share one and may be replayed side by
+    side, and a later call that needs more does not take it away."""
     if workspace is None:
+        if device.type == "cuda" and torch.cuda.is_current_stream_capturing():
+            return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
         return _get_workspace(device, kind, nbytes)
     _need(workspace, "workspace", torch.uint8, (workspace.numel(),), device)
     return workspace
@@ -223,13 +228,9 @@ def _workspace_for(device: torch.device, kind: str, nbytes: int,
 
 def _scratch_for(device: torch.device, kind: str, nbytes: int,
                  workspace: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
-    """_workspace_for, but nothing for no bytes, and a buffer of its own for a
-    call that is being captured: it then belongs to the graph, so that two
-    graphs never share one and may be replayed side by side."""
+    """_workspace_for, but nothing for no bytes."""
     if workspace is None and nbytes == 0:
         return None
-    if workspace is None and device.type == "cuda" and torch.cuda.is_current_stream_capturing():
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
     return _workspace_for(device, kind, nbytes, workspace)
 
 
