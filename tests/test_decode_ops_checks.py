@@ -297,3 +297,19 @@ def test_captured_calls_of_every_kind_own_their_workspace(lib, monkeypatch, kind
     a, b = (get(dev, kind, 512, None) for _ in range(2))
     assert a.numel() >= 512 and b.numel() >= 512 and a.data_ptr() != b.data_ptr()
     assert binding._workspace == {}
+
+
+def test_sample_between_rows_of_one_tensor(lib):  # noqa: F811
+    x = torch.zeros(3, 4, 50)
+    for i, j in ((0, 1), (1, 0), (3, 2), (0, 3)):   # disjoint rows of one buffer
+        assert _sample(logits=x[:, i], probs=x[:, j]).probs.data_ptr() == x[:, j].data_ptr()
+    n = len(lib.calls)
+    flat = torch.zeros(3, 200)
+    for logits, probs in ((x[:, 0], x[:, 0]), (flat[:, :50], flat[:, 49:99]),
+                          (flat[:, 101:151], flat[:, 150:])):
+        with pytest.raises(ValueError, match="overlap"):
+            _sample(logits=logits, probs=probs)
+    with pytest.raises(ValueError, match="overlap"):   # other steps: ranges decide
+        _sample(logits=flat.view(6, 100)[:3, :50], probs=flat[:, 50:100])
+    assert len(lib.calls) == n
+    _sample(R=2, V=0, probs=torch.zeros(2, 0))   # the library's to refuse

@@ -312,3 +312,12 @@ def test_entries_below_the_bound_in_its_step(cuda_device, T, p, dtype):
     logits[:, n * 255] = 30.0
     u = torch.rand(2, 5, generator=torch.Generator().manual_seed(4), dtype=torch.float64)
     _check(cuda_device, logits.to(dtype), u, T=[T] * 2, k=[200, 211], p=[p] * 2, exact=p == 1.0)
+
+
+def test_probabilities_beside_their_logits(cuda_device):
+    # both slices of one buffer: row r of one between rows of the other
+    logits, u = _logits(15, 7, 1001)
+    both = torch.full((7, 2, 1001), 9.0, device=cuda_device)
+    both[:, 0] = logits.to(cuda_device)
+    _check(cuda_device, both[:, 0], u, p=[0.9] * 7, probs=both[:, 1])
+    assert torch.equal(both[:, 0].cpu(), logits)

@@ -802,6 +802,16 @@ def _need_matrix(t: torch.Tensor, name: str, dtype: torch.dtype, shape: Tuple[in
     return shape[1]
 
 
+def _rows_apart(a: torch.Tensor, a_step: int, b: torch.Tensor, b_step: int) -> bool:
+    """Whether the rows of two matrices cannot meet although their ranges may:
+    equal steps, and the rows of one between those of the other (two slices of
+    one [R][n][V] tensor)."""
+    step, wide = a_step * a.element_size(), a.shape[1] * a.element_size()
+    if step == 0 or step != b_step * b.element_size():
+        return False
+    return wide <= (b.data_ptr() - a.data_ptr()) % step <= step - b.shape[1] * b.element_size()
+
+
 def sample(logits: torch.Tensor, u: torch.Tensor, temperature: Optional[torch.Tensor] = None,
            top_k: Optional[torch.Tensor] = None, top_p: Optional[torch.Tensor] = None,
            min_p: Optional[torch.Tensor] = None, tokens: Optional[torch.Tensor] = None,
@@ -842,7 +852,8 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature: Optional[torch.Te
     probs_ld = 0
     if probs is not None:
         probs_ld = _need_matrix(probs, "probs", torch.float32, (R, V), dev)
-        _apart(probs, "probs", logits)
+        if not _rows_apart(probs, probs_ld, logits, ld):
+            _apart(probs, "probs", logits)
     st = _status_for(dev, status)
     with _on(dev):
         rc = lib.tsd_sample(logits.data_ptr(), ld, dt, R, V, _ptr(temperature), _ptr(top_k),
