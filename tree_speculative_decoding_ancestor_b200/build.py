@@ -22,11 +22,11 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB_DIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIB_DIR, "libtsd.so")
-# The checked build (-DTSD_CHECKS): every global access whose index a kernel
-# computes is compared with its buffer's extent first; an index outside it
-# sets TSD_DEV_BOUNDS in the status word and the access is skipped.  Slower;
-# for small-case debugging.  Load it with TSD_LIBRARY=<path> before the
-# binding's first call.
+# The checked build (-DTSD_CHECKS): accesses to caches, logits, outputs and
+# partial results whose index a kernel computes are compared with their buffer's
+# extent first; an index outside it sets TSD_DEV_BOUNDS in the status word and
+# the access is skipped.  Slower; for small-case debugging.  Load it with
+# TSD_LIBRARY=<path> before the binding's first call.
 LIB_CHECKED = os.path.join(LIB_DIR, "libtsd_checked.so")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
